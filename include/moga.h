@@ -39,6 +39,9 @@
  *     memory.  In the default build such inputs are unchecked and their
  *     result is undefined.
  *   - Limits: N * H < 2^31, 1 <= M <= 32, d % 8 == 0, hd in {64, 128}.
+ *   - Beside the layer: the RMS norm with the residual's addition and the
+ *     gated feed-forward of the block around it (moga_rms_norm,
+ *     moga_gated_ffn and their backward calls, at the end).
  */
 #ifndef MOGA_H
 #define MOGA_H
@@ -60,7 +63,13 @@ typedef enum {
   MOGA_ERR_BAD_INDEX = 6
 } moga_status;
 
-typedef enum { MOGA_F32 = 0, MOGA_BF16 = 1 } moga_dtype;
+/* MOGA_E4M3: 8-bit floats (4 exponent and 3 mantissa bits, largest value 448),
+ * taken by the norm's output and the gated feed-forward only. */
+typedef enum { MOGA_F32 = 0, MOGA_BF16 = 1, MOGA_E4M3 = 2 } moga_dtype;
+
+/* Activations of the gated feed-forward: g / (1 + e^-g), and the tanh form
+ * 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))). */
+typedef enum { MOGA_ACT_SILU = 0, MOGA_ACT_GELU = 1 } moga_act;
 
 /* Static-group geometry (note, key design 4; translation, 时空分组注意力).
  * Tokens are in raster order t = frame*h*w + row*w + col.  Windows tile the
@@ -414,6 +423,86 @@ moga_status moga_sp_unpack_heads(const void* src, int64_t n, int32_t H, int32_t 
  * all-reduce) is L_gb.  loss: [1] double, written. */
 moga_status moga_balance_loss_part(const int32_t* counts, const void* route_ws, int64_t n_local, int64_t N,
                                    int32_t M, float alpha, double* loss, void* stream);
+
+/* ================================================= the block around the layer
+ * What a transformer block runs next to the attention layer: the norm in
+ * front of a projection, with the residual's addition, and the feed-forward
+ * half.  Conventions as above (device pointers, dense row-major, caller-owned
+ * buffers, asynchronous on `stream`, N >= 1). */
+
+/* Root-mean-square norm of N rows of d elements, with the residual's addition:
+ *   h = x + residual    (fp32 sum, rounded to the residual's type and stored;
+ *                        h = x where there is no residual)
+ *   y = h / sqrt(mean(h^2) + eps) * w          (fp32, rounded once)
+ * y is taken from the stored h.  An e4m3 output has one scale per row:
+ *   scale = max(max|y|, 2^-100) / 448,   y_q = e4m3(y / scale)
+ * and stands for y_q * scale.  A row with a NaN or an infinity in h gives NaN
+ * values (e4m3: the row's scale is NaN).
+ * x:        [N][d], x_dt (MOGA_F32 or MOGA_BF16)
+ * residual: [N][d], res_dt, or NULL.  Pairs (x, residual): bf16 + bf16,
+ *           bf16 + fp32, fp32 + fp32; fp32 + bf16 is MOGA_ERR_UNSUPPORTED
+ * w:        [d], w_dt (MOGA_F32 or MOGA_BF16)
+ * h:        [N][d], res_dt, out; NULL exactly where residual is NULL.  It may
+ *           be the residual's own buffer (the stream is then updated in place)
+ * y:        [N][d], y_dt: MOGA_BF16, MOGA_E4M3, or MOGA_F32 (with an fp32 h only,
+ *           else MOGA_ERR_UNSUPPORTED).  No other overlap with the inputs.
+ * scale:    [N] fp32 out with an e4m3 y, else NULL
+ * Requires d % 8 == 0, d <= 16384 (MOGA_ERR_UNSUPPORTED above), N < 2^30,
+ * eps > 0 and 16-byte aligned pointers.  Needs no workspace. */
+moga_status moga_rms_norm(const void* x, moga_dtype x_dt, const void* residual, moga_dtype res_dt,
+                          const void* w, moga_dtype w_dt, int64_t N, int32_t d, float eps, void* h,
+                          void* y, moga_dtype y_dt, float* scale, void* stream);
+
+/* Backward of moga_rms_norm.  With r = 1 / sqrt(mean(h^2) + eps), which is
+ * computed again from h, and dn = dy * w:
+ *   dx = r * (dn - h * r^2 * mean(dn * h)) + dres
+ *   dw = sum over rows of dy * h * r
+ * dx is the gradient of the stored sum h, so of x and of the residual alike.
+ * dy:        [N][d], dy_dt (an e4m3 y takes its gradient in bf16 or fp32)
+ * h:         [N][d], h_dt, as the forward stored it (x where it had no residual)
+ * dres:      [N][d], h_dt: gradient that reaches h past the norm, or NULL
+ * dx:        [N][d], h_dt, written; may be dres's own buffer
+ * dx_branch: [N][d] bf16, written: dx rounded for a bf16 x beside an fp32
+ *            residual; NULL to skip (and with a bf16 h)
+ * dw:        [d] fp32, written; NULL to skip
+ * ws:        moga_rms_norm_bwd_ws_bytes(N, d) bytes of scratch (unused, may be
+ *            NULL, where dw is NULL)
+ * fp32 dy with a bf16 h is MOGA_ERR_UNSUPPORTED; limits as for the forward.
+ * Deterministic: every sum runs in a fixed order. */
+size_t moga_rms_norm_bwd_ws_bytes(int64_t N, int32_t d);
+moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const void* h, moga_dtype h_dt, const void* w,
+                              moga_dtype w_dt, const void* dres, int64_t N, int32_t d, float eps, void* dx,
+                              void* dx_branch, float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/* Gated feed-forward: both projections, the activation and the product in one
+ * kernel,
+ *   out = act(x . W_gate^T) * (x . W_up^T)      (fp32, rounded to bf16 once)
+ * x:            [N][d], dt (MOGA_BF16 or MOGA_E4M3)
+ * w_gate, w_up: [F][d], dt (linear layers' weights)
+ * x_scale [N], w_gate_scale [F], w_up_scale [F]: fp32 with MOGA_E4M3, where a
+ *               row stands for its values times its scale (x and x_scale as
+ *               moga_rms_norm writes them); NULL with MOGA_BF16
+ * act:          MOGA_ACT_SILU or MOGA_ACT_GELU
+ * out:          [N][F] bf16, written
+ * Requires d % 8 == 0 (e4m3: d % 16 == 0), F % 8 == 0, d, F <= 2^20, N < 2^30
+ * and 16-byte aligned x, w_gate, w_up, out.  Needs no workspace. */
+moga_status moga_gated_ffn(const void* x, const void* w_gate, const void* w_up, moga_dtype dt,
+                           const float* x_scale, const float* w_gate_scale, const float* w_up_scale,
+                           int64_t N, int32_t d, int32_t F, int32_t act, void* out, void* stream);
+
+/* Backward of the bf16 moga_gated_ffn.  With g = x . W_gate^T, u = x . W_up^T
+ * computed again, dg = dout * u * act'(g) and du = dout * act(g), each rounded
+ * to bf16 for the products that follow:
+ *   dx = dg . W_gate + du . W_up,   dW_gate = dg^T . x,   dW_up = du^T . x
+ * dout: [N][F] bf16;  dx: [N][d] bf16, written, or NULL to skip;
+ * dw_gate, dw_up: [F][d] bf16, written, or both NULL to skip
+ * ws:   moga_gated_ffn_bwd_ws_bytes(N, d, F) bytes, 16-byte aligned (dg and
+ *       du).  Returns 0 for arguments the call would reject.
+ * Limits as for the bf16 forward. */
+size_t moga_gated_ffn_bwd_ws_bytes(int64_t N, int32_t d, int32_t F);
+moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, const void* w_up, int64_t N, int32_t d,
+                               int32_t F, int32_t act, const void* dout, void* dx, void* dw_gate, void* dw_up,
+                               void* ws, size_t ws_bytes, void* stream);
 
 /* ------------------------------------------------------------- diagnostics */
 /* Text of the last host-side error of the calling thread ("" if none). */

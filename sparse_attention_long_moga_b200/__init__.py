@@ -22,12 +22,14 @@ import math
 
 import torch
 
-from ._lib import MOGA_BF16, MOGA_F32, MogaError, StgaGeom, check, lib  # noqa: F401
+from ._lib import (MOGA_ACT_GELU, MOGA_ACT_SILU, MOGA_BF16, MOGA_E4M3, MOGA_F32, MogaError,  # noqa: F401
+                   StgaGeom, check, lib)
 
 __all__ = ["moga_route", "moga_permute", "moga_group_attn", "stga_attn", "stga_attn_train", "stga_attn_mean",
            "visual_attn_branches",
            "visual_attn_mean", "moga_balance_loss", "visual_attention_forward", "attn_workspace", "device_status",
-           "MogaError", "geom_struct", "visual_attention_forward_train", "visual_attention_backward"]
+           "MogaError", "geom_struct", "visual_attention_forward_train", "visual_attention_backward",
+           "moga_rms_norm", "moga_rms_norm_backward", "moga_gated_ffn", "moga_gated_ffn_backward"]
 
 
 def _ptr(t):
@@ -481,3 +483,151 @@ def visual_attention_backward(saved: dict, x, w_r, q, k, v, M: int, geom: dict, 
                            _ptr(saved["counts"]), alpha, dloss, _ptr(dx), _ptr(dw_r), _ptr(dbias), _ptr(rws),
                            rws.numel(), _stream()), "moga_route_bwd")
     return dict(dq=dq, dk=dk, dv=dv, dx=dx, dw_r=dw_r, dbias=dbias, dgate=dgate)
+
+
+# ---------------------------------------------------------------- the block around the layer
+#
+# The norm in front of a projection, with the residual's addition of a
+# branch's output, and the gated feed-forward half.  A block's forward is
+#
+#     y, h, _ = moga_rms_norm(attn_out, w_norm, residual=h)    # h: the stream
+#     a = moga_gated_ffn(y, w_gate, w_up)
+#     branch = a @ w_down.T                                    # the next norm adds it
+#
+# and in 8 bits y, h, s = moga_rms_norm(..., out_dtype=torch.float8_e4m3fn),
+# moga_gated_ffn(y, qg, qu, x_scale=s, w_gate_scale=..., w_up_scale=...).
+# N >= 1 rows, dense tensors.
+
+_NORM_DT = {torch.float32: MOGA_F32, torch.bfloat16: MOGA_BF16, torch.float8_e4m3fn: MOGA_E4M3}
+_ACTS = {"silu": MOGA_ACT_SILU, "gelu": MOGA_ACT_GELU}
+
+
+def _float_dt(t, name):
+    if t.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
+    return _NORM_DT[t.dtype]
+
+
+def moga_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
+                  out_dtype: torch.dtype = torch.bfloat16, h: torch.Tensor | None = None):
+    """h = x + residual (x without one), y = h / sqrt(mean(h^2) + eps) * weight over the rows of x [N, d].
+
+    x bf16 or fp32; residual bf16 (with a bf16 x) or fp32; weight [d] bf16 or fp32; out_dtype bf16,
+    float8_e4m3fn, or fp32 where the stream (residual, else x) is fp32.  Returns (y, h, scale): h in the
+    stream's dtype (x itself without a residual; the buffer `h` if given, which may be `residual`), and scale
+    fp32 [N] for an e4m3 y (a row stands for y * scale), else None."""
+    x_dt, w_dt = _float_dt(x, "x"), _float_dt(weight, "weight")
+    _need(x, x.dtype, "x", 2, device=False)
+    N, d = x.shape
+    _need(weight, weight.dtype, "weight", 1, (d,), device=False)
+    if out_dtype not in _NORM_DT:
+        raise ValueError("out_dtype must be bfloat16, float32 or float8_e4m3fn, got %s" % out_dtype)
+    r_dt = MOGA_F32
+    if residual is not None:
+        r_dt = _float_dt(residual, "residual")
+        _need(residual, residual.dtype, "residual", 2, (N, d), device=False)
+        if h is not None:
+            _need(h, residual.dtype, "h", 2, (N, d), device=False)
+    elif h is not None:
+        raise ValueError("h is the output of the residual's addition: there is no residual")
+    _on_device(x=x, weight=weight, residual=residual, h=h)
+    if residual is not None and h is None:
+        h = torch.empty_like(residual)
+    y = torch.empty((N, d), dtype=out_dtype, device=x.device)
+    scale = torch.empty(N, dtype=torch.float32, device=x.device) if out_dtype == torch.float8_e4m3fn else None
+    check(lib().moga_rms_norm(_ptr(x), x_dt, _ptr(residual), r_dt, _ptr(weight), w_dt, N, d, eps, _ptr(h), _ptr(y),
+                              _NORM_DT[out_dtype], _ptr(scale), _stream()), "moga_rms_norm")
+    return y, x if residual is None else h, scale
+
+
+def moga_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                           dres: torch.Tensor | None = None, eps: float = 1e-6,
+                           branch_dtype: torch.dtype | None = None, need_dw: bool = True,
+                           dx: torch.Tensor | None = None):
+    """Gradients of moga_rms_norm from dy [N, d], the stored h and dres (the gradient that reaches h past the
+    norm, h's dtype).  Returns (dx [N, d] in h's dtype, dw fp32 [d] or None, dx_branch): dx is the gradient of x
+    and of the residual alike, in the buffer `dx` if given (which may be dres); branch_dtype=torch.bfloat16 with an
+    fp32 h also gives it rounded for the bf16 branch, else dx_branch is None."""
+    dy_dt, h_dt, w_dt = _float_dt(dy, "dy"), _float_dt(h, "h"), _float_dt(weight, "weight")
+    _need(h, h.dtype, "h", 2, device=False)
+    N, d = h.shape
+    _need(dy, dy.dtype, "dy", 2, (N, d), device=False)
+    _need(weight, weight.dtype, "weight", 1, (d,), device=False)
+    if dres is not None:
+        _need(dres, h.dtype, "dres", 2, (N, d), device=False)
+    if dx is not None:
+        _need(dx, h.dtype, "dx", 2, (N, d), device=False)
+    if branch_dtype not in (None, torch.bfloat16):
+        raise ValueError("branch_dtype must be None or bfloat16, got %s" % branch_dtype)
+    _on_device(dy=dy, h=h, weight=weight, dres=dres, dx=dx)
+    L = lib()
+    dev = h.device
+    if dx is None:
+        dx = torch.empty_like(h)
+    dxb = torch.empty((N, d), dtype=torch.bfloat16, device=dev) if branch_dtype is not None else None
+    dw = ws = None
+    if need_dw:
+        dw = torch.empty(d, dtype=torch.float32, device=dev)
+        ws = torch.empty(max(L.moga_rms_norm_bwd_ws_bytes(N, d), 16), dtype=torch.uint8, device=dev)
+    check(L.moga_rms_norm_bwd(_ptr(dy), dy_dt, _ptr(h), h_dt, _ptr(weight), w_dt, _ptr(dres), N, d, eps, _ptr(dx),
+                              _ptr(dxb), _ptr(dw), _ptr(ws), ws.numel() if need_dw else 0, _stream()),
+          "moga_rms_norm_bwd")
+    return dx, dw, dxb
+
+
+def _check_ffn(x, w_gate, w_up, act):
+    if act not in _ACTS:
+        raise ValueError("act must be 'silu' or 'gelu', got %r" % (act,))
+    _need(x, x.dtype, "x", 2, device=False)
+    N, d = x.shape
+    _need(w_gate, x.dtype, "w_gate", 2, device=False)
+    if w_gate.shape[1] != d:
+        raise ValueError("w_gate must be [F, d] with x's d=%d, got %s" % (d, tuple(w_gate.shape)))
+    F = w_gate.shape[0]
+    _need(w_up, x.dtype, "w_up", 2, (F, d), device=False)
+    return N, d, F
+
+
+def moga_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, act: str = "silu",
+                   x_scale: torch.Tensor | None = None, w_gate_scale: torch.Tensor | None = None,
+                   w_up_scale: torch.Tensor | None = None):
+    """act(x w_gate^T) * (x w_up^T) -> bf16 [N, F], both projections in one kernel.
+
+    x [N, d], w_gate, w_up [F, d]: bf16, or float8_e4m3fn with fp32 scales x_scale [N], w_gate_scale [F],
+    w_up_scale [F] (a row stands for its values times its scale).  act: "silu" or "gelu" (tanh form)."""
+    if x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError("x must be bfloat16 or float8_e4m3fn, got %s" % x.dtype)
+    N, d, F = _check_ffn(x, w_gate, w_up, act)
+    scales = (("x_scale", x_scale, N), ("w_gate_scale", w_gate_scale, F), ("w_up_scale", w_up_scale, F))
+    for name, t, n in scales:
+        if x.dtype == torch.bfloat16:
+            if t is not None:
+                raise ValueError("%s goes with float8_e4m3fn operands" % name)
+        elif t is None:
+            raise ValueError("float8_e4m3fn operands need %s" % name)
+        else:
+            _need(t, torch.float32, name, 1, (n,), device=False)
+    _on_device(x=x, w_gate=w_gate, w_up=w_up, x_scale=x_scale, w_gate_scale=w_gate_scale, w_up_scale=w_up_scale)
+    out = torch.empty((N, F), dtype=torch.bfloat16, device=x.device)
+    check(lib().moga_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _NORM_DT[x.dtype], _ptr(x_scale),
+                               _ptr(w_gate_scale), _ptr(w_up_scale), N, d, F, _ACTS[act], _ptr(out), _stream()),
+          "moga_gated_ffn")
+    return out
+
+
+def moga_gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, dout: torch.Tensor,
+                            act: str = "silu", need_dx: bool = True, need_dw: bool = True):
+    """Gradients of the bf16 moga_gated_ffn from dout [N, F] bf16: dict(dx [N, d], dw_gate, dw_up [F, d]), bf16
+    (None where not asked for).  Both projections are computed again, so the forward saves nothing but x."""
+    _need(x, torch.bfloat16, "x", 2, device=False)
+    N, d, F = _check_ffn(x, w_gate, w_up, act)
+    _need(dout, torch.bfloat16, "dout", 2, (N, F), device=False)
+    _on_device(x=x, w_gate=w_gate, w_up=w_up, dout=dout)
+    L = lib()
+    b16 = dict(dtype=torch.bfloat16, device=x.device)
+    dx = torch.empty((N, d), **b16) if need_dx else None
+    dwg, dwu = (torch.empty((F, d), **b16) if need_dw else None for _ in range(2))
+    ws = torch.empty(max(L.moga_gated_ffn_bwd_ws_bytes(N, d, F), 16), dtype=torch.uint8, device=x.device)
+    check(L.moga_gated_ffn_bwd(_ptr(x), _ptr(w_gate), _ptr(w_up), N, d, F, _ACTS[act], _ptr(dout), _ptr(dx),
+                               _ptr(dwg), _ptr(dwu), _ptr(ws), ws.numel(), _stream()), "moga_gated_ffn_bwd")
+    return dict(dx=dx, dw_gate=dwg, dw_up=dwu)

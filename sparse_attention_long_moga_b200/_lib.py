@@ -19,7 +19,8 @@ DEBUG_LIB_PATH = os.path.join(PKG, "libmoga_debug.so")
 
 STATUS = {0: "MOGA_OK", 1: "MOGA_ERR_INVALID_ARG", 2: "MOGA_ERR_UNSUPPORTED", 3: "MOGA_ERR_WORKSPACE",
           4: "MOGA_ERR_CUDA", 5: "MOGA_ERR_TIMEOUT", 6: "MOGA_ERR_BAD_INDEX"}
-MOGA_F32, MOGA_BF16 = 0, 1
+MOGA_F32, MOGA_BF16, MOGA_E4M3 = 0, 1, 2
+MOGA_ACT_SILU, MOGA_ACT_GELU = 0, 1
 
 # exported symbol -> (restype, argtypes); the same list include/moga.h declares
 _P, _I32, _I64, _F32, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
@@ -62,6 +63,14 @@ SIGNATURES = {
     "moga_route_bwd_ws_bytes": (_SZ, [_I64, _I32, _I32]),
     "moga_route_bwd": (ctypes.c_int, [_P, _P, ctypes.c_int, _I64, _I32, _I32, _P, _P, _P, _P, _F32, _F32, _P, _P, _P,
                                       _P, _SZ, _P]),
+    "moga_rms_norm": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int, _P, ctypes.c_int, _I64, _I32, _F32, _P, _P,
+                                     ctypes.c_int, _P, _P]),
+    "moga_rms_norm_bwd_ws_bytes": (_SZ, [_I64, _I32]),
+    "moga_rms_norm_bwd": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int, _P, ctypes.c_int, _P, _I64, _I32, _F32,
+                                         _P, _P, _P, _P, _SZ, _P]),
+    "moga_gated_ffn": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _P, _P, _P, _I64, _I32, _I32, _I32, _P, _P]),
+    "moga_gated_ffn_bwd_ws_bytes": (_SZ, [_I64, _I32, _I32]),
+    "moga_gated_ffn_bwd": (ctypes.c_int, [_P, _P, _P, _I64, _I32, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P]),
     "moga_last_error": (ctypes.c_char_p, []),
     "moga_device_status": (ctypes.c_int, [_P]),
     "moga_version": (ctypes.c_char_p, []),

@@ -16,7 +16,7 @@ LIB = os.path.join(PKG, "libmoga.so")
 # the checking build: device-side index checks (-DMOGA_DEBUG), same ABI
 DEBUG_LIB = os.path.join(PKG, "libmoga_debug.so")
 SOURCES = ["moga_lib.cu"]
-DEPS = ["tc_common.cuh", "route_tc.cu", "route_bwd.cu", "sp.cu", "qkv_route.cu", "attention_bwd.cu", "api_common.cu", "route.cu", "permute.cu", "permute_noalloc.cu", "mean_loss.cu", "attention.cu", "common.cuh"]
+DEPS = ["tc_common.cuh", "rms_norm.cu", "gated_ffn.cu", "route_tc.cu", "route_bwd.cu", "sp.cu", "qkv_route.cu", "attention_bwd.cu", "api_common.cu", "route.cu", "permute.cu", "permute_noalloc.cu", "mean_loss.cu", "attention.cu", "common.cuh"]
 
 
 def nvcc() -> str:

@@ -10,3 +10,5 @@
 #include "route_bwd.cu"
 #include "sp.cu"
 #include "qkv_route.cu"
+#include "rms_norm.cu"
+#include "gated_ffn.cu"

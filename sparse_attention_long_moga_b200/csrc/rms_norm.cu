@@ -1,0 +1,545 @@
+// Root-mean-square norm with the residual's addition, and its backward.
+//
+// Forward, per row of d elements:
+//   h = x + residual                (rounded to the stream's type and stored)
+//   r = 1 / sqrt(mean(h^2) + eps),  y = h * r * w
+// y is taken from the stored h, so that the backward, which reads only h,
+// differentiates exactly what the forward computed.  The 8-bit output is
+//   scale = max(max|y|, 2^-100) / 448,  q = e4m3(y / scale)  per row;
+// y / scale = (h w) * 448 / max|h w| (r cancels), which needs one rounding
+// fewer and keeps q off the wrong side of a rounding border.
+//
+// Backward, with dn = dy * w and c = r^2 * mean(dn * h):
+//   dx = r * (dn - h * c) + dres,   dw = sum over rows of dy * h * r
+// r is recomputed: the row is in registers anyway, so nothing is saved but h.
+//
+// Bound: HBM.  Each row is read once into registers (8-element vectors, one
+// to five per thread) and written once; sums, the row statistics and dw are
+// fp32.  TPR threads share a row, 256 / TPR rows share a CTA.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+
+namespace moga {
+namespace norm {
+
+constexpr float kE4m3Max = 448.f;
+constexpr float kScaleFloor = 7.888609052210118e-31f;   // 2^-100
+constexpr int kMaxD = 16384;
+
+
+template <class T> struct Vec;
+template <> struct Vec<__nv_bfloat16> {
+  using type = uint4;
+  static __device__ __forceinline__ type load(const __nv_bfloat16* p) { return *reinterpret_cast<const uint4*>(p); }
+  static __device__ __forceinline__ void widen(const type& t, float* f) {
+    const uint32_t u[4] = {t.x, t.y, t.z, t.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(u[i] << 16);
+      f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+    }
+  }
+  // rounds to nearest even; f becomes the stored value
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+  static __device__ __forceinline__ float round(float f) { return __bfloat162float(__float2bfloat16_rn(f)); }
+};
+template <> struct Vec<float> {
+  struct type { float4 a, b; };
+  static __device__ __forceinline__ type load(const float* p) {
+    return {*reinterpret_cast<const float4*>(p), *reinterpret_cast<const float4*>(p + 4)};
+  }
+  static __device__ __forceinline__ void widen(const type& t, float* f) {
+    f[0] = t.a.x; f[1] = t.a.y; f[2] = t.a.z; f[3] = t.a.w;
+    f[4] = t.b.x; f[5] = t.b.y; f[6] = t.b.z; f[7] = t.b.w;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* f) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  }
+  static __device__ __forceinline__ float round(float f) { return f; }
+};
+template <> struct Vec<__nv_fp8_e4m3> {
+  // values already scaled into +-448; out of range saturates, NaN stays NaN
+  static __device__ __forceinline__ void store(__nv_fp8_e4m3* p, const float* f) {
+    uint32_t u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i], f[4 * i + 1]), __NV_SATFINITE, __NV_E4M3);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(f[4 * i + 2], f[4 * i + 3]), __NV_SATFINITE, __NV_E4M3);
+      u[i] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[1]);
+  }
+};
+
+// 8 weights of either type as fp32 (w is small and stays in L1)
+__device__ __forceinline__ void load_w(const void* w, bool w_bf16, int col, float* f) {
+  if (w_bf16) {
+    Vec<__nv_bfloat16>::widen(Vec<__nv_bfloat16>::load(static_cast<const __nv_bfloat16*>(w) + col), f);
+  } else {
+    Vec<float>::widen(Vec<float>::load(static_cast<const float*>(w) + col), f);
+  }
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// Barrier of the TPR threads of one row (named barrier 1 + group).
+template <int TPR>
+__device__ __forceinline__ void row_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TPR) : "memory");
+}
+
+// Sum (or maximum) over the TPR threads of a row, in the same order on every
+// thread.  `slots`: TPR / 32 floats of the row's own that no thread still
+// reads; consecutive calls take different slots.
+template <int TPR, bool MAX>
+__device__ __forceinline__ float row_reduce(float v, float* slots, int group, int lane_in_row) {
+  v = MAX ? warp_max(v) : warp_sum(v);
+  if (TPR == 32) return v;
+  if ((lane_in_row & 31) == 0) slots[lane_in_row >> 5] = v;
+  row_sync<TPR>(group);
+  float r = slots[0];
+#pragma unroll
+  for (int i = 1; i < TPR / 32; ++i) r = MAX ? fmaxf(r, slots[i]) : r + slots[i];
+  return r;
+}
+
+struct FwdParams {
+  const void *x, *res, *w;
+  void *h, *y;
+  float* scale;
+  int N, d;
+  float eps;
+  bool w_bf16;
+};
+
+template <int TPR>
+constexpr int kCtaThreads = TPR > 256 ? TPR : 256;
+
+template <int TPR, int VPT, class XT, class HT, bool RES, class YT>
+__global__ void __launch_bounds__(kCtaThreads<TPR>)
+rms_norm_kernel(const FwdParams p) {
+  constexpr int kGroups = kCtaThreads<TPR> / TPR;
+  constexpr bool kQuant = sizeof(YT) == 1;
+  __shared__ float red[2][kGroups][TPR / 32];
+  const int group = threadIdx.x / TPR, li = threadIdx.x % TPR;
+  const int row = blockIdx.x * kGroups + group;
+  if (row >= p.N) return;   // whole rows leave together: the row barriers stay complete
+  const int nv = p.d >> 3;
+  const size_t base = (size_t)row * p.d;
+  float f[VPT][8];
+  typename Vec<XT>::type xv[VPT];
+  typename Vec<HT>::type rv[VPT];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = li + i * TPR;
+    if (v < nv) {
+      xv[i] = Vec<XT>::load(static_cast<const XT*>(p.x) + base + 8 * v);
+      if (RES) rv[i] = Vec<HT>::load(static_cast<const HT*>(p.res) + base + 8 * v);
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = li + i * TPR;
+    if (v < nv) {
+      Vec<XT>::widen(xv[i], f[i]);
+      if (RES) {
+        float r[8];
+        Vec<HT>::widen(rv[i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = Vec<HT>::round(f[i][j] + r[j]);
+        Vec<HT>::store(static_cast<HT*>(p.h) + base + 8 * v, f[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss += f[i][j] * f[i][j];
+    }
+  }
+  ss = row_reduce<TPR, false>(ss, red[0][group], group, li);
+  const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
+  float mx = 0.f;
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = li + i * TPR;
+    if (v < nv) {
+      float w[8];
+      load_w(p.w, p.w_bf16, 8 * v, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        f[i][j] = kQuant ? f[i][j] * w[j] : f[i][j] * rstd * w[j];
+        if (kQuant) mx = fmaxf(mx, fabsf(f[i][j]));
+      }
+      if (!kQuant) Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, f[i]);
+    }
+  }
+  if (kQuant) {
+    mx = row_reduce<TPR, true>(mx, red[1][group], group, li);
+    const float amax = mx * rstd;                             // max|y|; NaN if the row holds NaN or infinity
+    const float top = amax < kScaleFloor ? kScaleFloor : amax;
+    // the short way where neither 448 / max|h w| nor the floor matters
+    const bool direct = amax >= kScaleFloor && mx >= kScaleFloor;
+    const float k1 = direct ? 1.f : rstd, k2 = kE4m3Max / (direct ? mx : top);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (v < nv) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = (f[i][j] * k1) * k2;
+        Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, f[i]);
+      }
+    }
+    if (li == 0) p.scale[row] = top / kE4m3Max;
+  }
+}
+
+struct BwdParams {
+  const void *dy, *h, *w, *dres;
+  void* dx;
+  __nv_bfloat16* dx_branch;
+  float* partial;    // [gridDim.x][d] sums of dy * h * r, or NULL
+  int N, d;
+  float eps;
+  bool w_bf16;
+};
+
+// Persistent: a CTA walks its rows with a fixed stride and keeps its share of
+// dw in registers (each thread always sees the same columns), then adds its
+// row groups in shared memory and writes one partial row.  No atomics: every
+// sum runs in a fixed order, so dw is the same from run to run.
+template <int TPR, int VPT, class DT, class HT>
+__global__ void __launch_bounds__(kCtaThreads<TPR>)
+rms_norm_bwd_kernel(const BwdParams p) {
+  constexpr int kGroups = kCtaThreads<TPR> / TPR;
+  extern __shared__ float s_dw[];                 // [d] when there is more than one group
+  __shared__ float red[2][2][kGroups][TPR / 32];
+  const int group = threadIdx.x / TPR, li = threadIdx.x % TPR;
+  const int nv = p.d >> 3;
+  float acc[VPT][8];
+#pragma unroll
+  for (int i = 0; i < VPT; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  int par = 0;
+  for (int row = blockIdx.x * kGroups + group; row < p.N; row += gridDim.x * kGroups, par ^= 1) {
+    const size_t base = (size_t)row * p.d;
+    typename Vec<DT>::type dv[VPT];
+    typename Vec<HT>::type hv[VPT], sv[VPT];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (v < nv) {
+        dv[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
+        hv[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
+        if (p.dres) sv[i] = Vec<HT>::load(static_cast<const HT*>(p.dres) + base + 8 * v);
+      }
+    }
+    float ss = 0.f, dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (v < nv) {
+        float dy[8], h[8], w[8];
+        Vec<DT>::widen(dv[i], dy);
+        Vec<HT>::widen(hv[i], h);
+        load_w(p.w, p.w_bf16, 8 * v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          ss += h[j] * h[j];
+          dot += dy[j] * w[j] * h[j];
+        }
+      }
+    }
+    // both sums cross one barrier
+    ss = warp_sum(ss);
+    dot = warp_sum(dot);
+    if (TPR > 32) {
+      float* s0 = red[par][0][group];
+      float* s1 = red[par][1][group];
+      if ((li & 31) == 0) {
+        s0[li >> 5] = ss;
+        s1[li >> 5] = dot;
+      }
+      row_sync<TPR>(group);
+      ss = s0[0];
+      dot = s1[0];
+#pragma unroll
+      for (int i = 1; i < TPR / 32; ++i) {
+        ss += s0[i];
+        dot += s1[i];
+      }
+    }
+    const float inv_d = 1.f / (float)p.d;
+    const float rstd = 1.f / sqrtf(ss * inv_d + p.eps);
+    const float c = rstd * rstd * (dot * inv_d);
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (v < nv) {
+        float dy[8], h[8], w[8], o[8];
+        Vec<DT>::widen(dv[i], dy);
+        Vec<HT>::widen(hv[i], h);
+        load_w(p.w, p.w_bf16, 8 * v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          o[j] = rstd * (dy[j] * w[j] - h[j] * c);
+          acc[i][j] += dy[j] * (h[j] * rstd);
+        }
+        if (p.dres) {
+          float s[8];
+          Vec<HT>::widen(sv[i], s);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] += s[j];
+        }
+        Vec<HT>::store(static_cast<HT*>(p.dx) + base + 8 * v, o);
+        if (p.dx_branch) Vec<__nv_bfloat16>::store(p.dx_branch + base + 8 * v, o);
+      }
+    }
+  }
+  if (!p.partial) return;
+  float* dst = p.partial + (size_t)blockIdx.x * p.d;
+  for (int g = 0; g < kGroups; ++g) {
+    if (group == g) {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = li + i * TPR;
+        if (v < nv) {
+          if (g > 0) {
+            float s[8];
+            Vec<float>::widen(Vec<float>::load(s_dw + 8 * v), s);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] += s[j];
+          }
+          Vec<float>::store(g == kGroups - 1 ? dst + 8 * v : s_dw + 8 * v, acc[i]);
+        }
+      }
+    }
+    if (kGroups > 1) __syncthreads();
+  }
+}
+
+// dw[c] = sum of the partial rows: 32 columns a CTA, 32 strided row slices
+// added in order.
+__global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restrict__ partial, int rows, int d,
+                                                           float* __restrict__ dw) {
+  __shared__ float s[32][33];
+  const int c = blockIdx.x * 32 + threadIdx.x, j = threadIdx.y;
+  float a = 0.f;
+  if (c < d)
+    for (int r = j; r < rows; r += 32) a += partial[(size_t)r * d + c];
+  s[j][threadIdx.x] = a;
+  __syncthreads();
+  if (j == 0 && c < d) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
+    dw[c] = t;
+  }
+}
+
+// (threads a row, vectors a thread): the first whose capacity holds the row.
+// f gets the index.  For few rows (below `wide_rows`) a row's own latency
+// counts, not the lanes left idle, so wider rows are taken.
+inline int pick_config(int d, int64_t N, int wide_rows) {
+  static const int cap[6] = {32 * 3, 64 * 3, 64 * 5, 128 * 5, 256 * 5, 512 * 5};
+  const int nv = d >> 3;
+  int i = 0;
+  while (cap[i] < nv) ++i;
+  if (N <= wide_rows) {
+    static const int one[6] = {32, 64, 64, 128, 256, 512};
+    while (i < 5 && one[i] < nv) ++i;
+  }
+  return i;
+}
+
+inline int sm_count_of_current() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 148;
+  return n > 0 ? n : 148;
+}
+
+template <class XT, class HT, bool RES, class YT>
+static moga_status launch_fwd(const FwdParams& p, cudaStream_t s) {
+  switch (pick_config(p.d, p.N, sm_count_of_current())) {
+#define MOGA_NORM_CASE(I, TPR, VPT)                                                                            \
+  case I: {                                                                                                    \
+    constexpr int g = kCtaThreads<TPR> / TPR;                                                                \
+    rms_norm_kernel<TPR, VPT, XT, HT, RES, YT><<<(p.N - 1) / g + 1, kCtaThreads<TPR>, 0, s>>>(p);            \
+    break;                                                                                                     \
+  }
+    MOGA_NORM_CASE(0, 32, 3)
+    MOGA_NORM_CASE(1, 64, 3)
+    MOGA_NORM_CASE(2, 64, 5)
+    MOGA_NORM_CASE(3, 128, 5)
+    MOGA_NORM_CASE(4, 256, 5)
+    MOGA_NORM_CASE(5, 512, 5)
+#undef MOGA_NORM_CASE
+  }
+  return check_launch("moga_rms_norm");
+}
+
+template <class XT, class HT, bool RES>
+static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_t s) {
+  if (y_dt == MOGA_E4M3) return launch_fwd<XT, HT, RES, __nv_fp8_e4m3>(p, s);
+  if (y_dt == MOGA_BF16) return launch_fwd<XT, HT, RES, __nv_bfloat16>(p, s);
+  if constexpr (sizeof(HT) == 4) return launch_fwd<XT, HT, RES, float>(p, s);
+  return fail(MOGA_ERR_UNSUPPORTED, "moga_rms_norm: an fp32 output needs an fp32 stream");
+}
+
+inline int bwd_groups(int cfg) {
+  static const int g[6] = {8, 4, 4, 2, 1, 1};
+  return g[cfg];
+}
+// CTAs of the backward: enough for two per SM, at most one per row group.
+inline int bwd_ctas(int64_t N, int d, int sms) {
+  const int g = bwd_groups(pick_config(d, N, 0));
+  const int64_t want = (N + g - 1) / g;
+  return (int)(want < 2 * (int64_t)sms ? want : 2 * (int64_t)sms);
+}
+
+template <class DT, class HT>
+static moga_status launch_bwd(const BwdParams& p, int ctas, cudaStream_t s) {
+  switch (pick_config(p.d, p.N, 0)) {
+#define MOGA_NORM_CASE(I, TPR, VPT)                                                                         \
+  case I: {                                                                                                 \
+    constexpr int g = kCtaThreads<TPR> / TPR;                                                             \
+    const size_t smem = g > 1 ? (size_t)p.d * sizeof(float) : 0;                                            \
+    rms_norm_bwd_kernel<TPR, VPT, DT, HT><<<ctas, kCtaThreads<TPR>, smem, s>>>(p);                        \
+    break;                                                                                                  \
+  }
+    MOGA_NORM_CASE(0, 32, 3)
+    MOGA_NORM_CASE(1, 64, 3)
+    MOGA_NORM_CASE(2, 64, 5)
+    MOGA_NORM_CASE(3, 128, 5)
+    MOGA_NORM_CASE(4, 256, 5)
+    MOGA_NORM_CASE(5, 512, 5)
+#undef MOGA_NORM_CASE
+  }
+  return check_launch("moga_rms_norm_bwd");
+}
+
+static moga_status check_dims(const char* who, int64_t N, int32_t d, float eps) {
+  if (N <= 0 || N > INT32_MAX / 2) return fail(MOGA_ERR_INVALID_ARG, "%s: N=%lld out of range", who, (long long)N);
+  if (d <= 0 || d % 8 != 0) return fail(MOGA_ERR_INVALID_ARG, "%s: d=%d must be a positive multiple of 8", who, d);
+  if (d > kMaxD) return fail(MOGA_ERR_UNSUPPORTED, "%s: d=%d above %d", who, d, kMaxD);
+  if (!(eps > 0.f && eps < 1e30f)) return fail(MOGA_ERR_INVALID_ARG, "%s: eps must be positive and finite", who);
+  return MOGA_OK;
+}
+
+inline bool is_float_dt(moga_dtype t) { return t == MOGA_F32 || t == MOGA_BF16; }
+
+}  // namespace norm
+}  // namespace moga
+
+extern "C" moga_status moga_rms_norm(const void* x, moga_dtype x_dt, const void* residual, moga_dtype res_dt,
+                                     const void* w, moga_dtype w_dt, int64_t N, int32_t d, float eps, void* h,
+                                     void* y, moga_dtype y_dt, float* scale, void* stream) {
+  using namespace moga;
+  using namespace moga::norm;
+  if (!x || !w || !y) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: null pointer");
+  if ((residual != nullptr) != (h != nullptr))
+    return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: residual and h go together");
+  if (!is_float_dt(x_dt) || !is_float_dt(w_dt) || (residual && !is_float_dt(res_dt)) ||
+      (!is_float_dt(y_dt) && y_dt != MOGA_E4M3))
+    return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: bad dtype");
+  if ((y_dt == MOGA_E4M3) != (scale != nullptr))
+    return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: scale goes with an e4m3 output");
+  moga_status st = check_dims("moga_rms_norm", N, d, eps);
+  if (st != MOGA_OK) return st;
+  if (residual && x_dt == MOGA_F32 && res_dt == MOGA_BF16)
+    return fail(MOGA_ERR_UNSUPPORTED, "moga_rms_norm: an fp32 x needs an fp32 residual");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
+                      reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(h);
+  if ((a & 15) || (reinterpret_cast<uintptr_t>(y) & 15) || (reinterpret_cast<uintptr_t>(scale) & 3))
+    return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: pointers must be 16-byte aligned");
+  norm::FwdParams p;
+  p.x = x;
+  p.res = residual;
+  p.w = w;
+  p.h = h;
+  p.y = y;
+  p.scale = scale;
+  p.N = (int)N;
+  p.d = d;
+  p.eps = eps;
+  p.w_bf16 = w_dt == MOGA_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  using B = __nv_bfloat16;
+  if (!residual)
+    return x_dt == MOGA_BF16 ? launch_fwd_y<B, B, false>(p, y_dt, s) : launch_fwd_y<float, float, false>(p, y_dt, s);
+  if (res_dt == MOGA_BF16) return launch_fwd_y<B, B, true>(p, y_dt, s);
+  return x_dt == MOGA_BF16 ? launch_fwd_y<B, float, true>(p, y_dt, s) : launch_fwd_y<float, float, true>(p, y_dt, s);
+}
+
+extern "C" size_t moga_rms_norm_bwd_ws_bytes(int64_t N, int32_t d) {
+  using namespace moga::norm;
+  if (N <= 0 || N > INT32_MAX / 2 || d <= 0 || d % 8 != 0 || d > kMaxD) return 0;
+  return (size_t)bwd_ctas(N, d, sm_count_of_current()) * d * sizeof(float);
+}
+
+extern "C" moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const void* h, moga_dtype h_dt,
+                                         const void* w, moga_dtype w_dt, const void* dres, int64_t N, int32_t d,
+                                         float eps, void* dx, void* dx_branch, float* dw, void* ws, size_t ws_bytes,
+                                         void* stream) {
+  using namespace moga;
+  using namespace moga::norm;
+  if (!dy || !h || !w || !dx) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: null pointer");
+  if (!is_float_dt(dy_dt) || !is_float_dt(h_dt) || !is_float_dt(w_dt))
+    return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: bad dtype");
+  moga_status st = check_dims("moga_rms_norm_bwd", N, d, eps);
+  if (st != MOGA_OK) return st;
+  if (dy_dt == MOGA_F32 && h_dt == MOGA_BF16)
+    return fail(MOGA_ERR_UNSUPPORTED, "moga_rms_norm_bwd: an fp32 dy needs an fp32 h");
+  if (dx_branch && h_dt == MOGA_BF16)
+    return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: dx_branch is for an fp32 h (dx is bf16 already)");
+  const uintptr_t a = reinterpret_cast<uintptr_t>(dy) | reinterpret_cast<uintptr_t>(h) |
+                      reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(dres) |
+                      reinterpret_cast<uintptr_t>(dx) | reinterpret_cast<uintptr_t>(dx_branch) |
+                      reinterpret_cast<uintptr_t>(dw) | reinterpret_cast<uintptr_t>(ws);
+  if (a & 15) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: pointers must be 16-byte aligned");
+  const int ctas = bwd_ctas(N, d, sm_count_of_current());
+  if (dw) {
+    const size_t need = (size_t)ctas * d * sizeof(float);
+    if (!ws) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: null workspace");
+    if (ws_bytes < need)
+      return fail(MOGA_ERR_WORKSPACE, "moga_rms_norm_bwd: workspace %zu < %zu bytes", ws_bytes, need);
+  }
+  norm::BwdParams p;
+  p.dy = dy;
+  p.h = h;
+  p.w = w;
+  p.dres = dres;
+  p.dx = dx;
+  p.dx_branch = static_cast<__nv_bfloat16*>(dx_branch);
+  p.partial = dw ? static_cast<float*>(ws) : nullptr;
+  p.N = (int)N;
+  p.d = d;
+  p.eps = eps;
+  p.w_bf16 = w_dt == MOGA_BF16;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  using B = __nv_bfloat16;
+  if (h_dt == MOGA_BF16) st = launch_bwd<B, B>(p, ctas, s);
+  else if (dy_dt == MOGA_BF16) st = launch_bwd<B, float>(p, ctas, s);
+  else st = launch_bwd<float, float>(p, ctas, s);
+  if (st != MOGA_OK || !dw) return st;
+  rms_norm_dw_kernel<<<ceil_div(d, 32), dim3(32, 32), 0, s>>>(p.partial, ctas, d, dw);
+  return check_launch("moga_rms_norm_bwd/dw");
+}
