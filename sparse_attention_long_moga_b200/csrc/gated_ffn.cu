@@ -344,6 +344,141 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap
   if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
 }
 
+// ---------------------------------------------------------------- few tokens
+//
+// Up to kFewTokens tokens the weights' read is the time (2 F d elements for
+// N d + N F others), and a 256-row tile would idle.  A CTA takes 8 RT columns
+// of F and all tokens; its 8 warps split d, each streaming 64-byte pieces of
+// 16 RT weight rows straight from global memory into mma.sync fragments: one
+// 16-row A tile is 8 gate rows over the 8 up rows of the same columns, so a
+// lane's accumulators hold gate and up of the same outputs.  A lane loads 16
+// consecutive bytes of a row where the fragment wants four pieces spread over
+// k; the sum over k does not mind the order as long as x is read in the same
+// one.  No shared-memory stage, no barrier in the loop: with UN steps unrolled
+// a lane keeps 2 RT UN 16-byte loads in flight.  The warps' sums meet in
+// shared memory in a fixed order.
+constexpr int kFewTokens = 32;
+
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
+}
+// D += A (16 rows x 32 bytes of k) B (8 columns): one legacy tensor-core step
+template <bool E4M3>
+__device__ __forceinline__ void mma_16x8(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if (E4M3)
+    asm volatile("mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                 "{%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct FewParams {
+  const uint8_t *x, *wg, *wu;   // rows of `row_bytes` bytes
+  int N, F, row_bytes;
+  const float *xs, *gs, *us;
+  __nv_bfloat16* out;
+};
+
+template <bool E4M3, int ACT, int RT, int NT, int UN>
+__global__ void __launch_bounds__(256) ffn_few_kernel(const FewParams p) {
+  constexpr int kCols = 8 * RT, kToks = 8 * NT;
+  __shared__ float red[8][RT * NT * 4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int f0 = blockIdx.x * kCols;
+  const uint8_t *wg[RT], *wu[RT], *xp[NT];
+  bool won[RT], xon[NT];
+#pragma unroll
+  for (int r = 0; r < RT; ++r) {
+    const int f = f0 + 8 * r + g;
+    won[r] = f < p.F;
+    wg[r] = p.wg + (size_t)(won[r] ? f : 0) * p.row_bytes + 16 * q;
+    wu[r] = p.wu + (size_t)(won[r] ? f : 0) * p.row_bytes + 16 * q;
+  }
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    xon[n] = 8 * n + g < p.N;
+    xp[n] = p.x + (size_t)(xon[n] ? 8 * n + g : 0) * p.row_bytes + 16 * q;
+  }
+  float acc[RT][NT][4];
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  // step s covers bytes [64 s, 64 s + 64) of every row; warp w takes s = w, w + 8, ...
+  for (int s0 = warp; 64 * s0 < p.row_bytes; s0 += 8 * UN) {
+    uint4 a[UN][RT], b[UN][RT], x[UN][NT];
+#pragma unroll
+    for (int i = 0; i < UN; ++i) {
+      const int k = 64 * (s0 + 8 * i);
+      const bool on = k + 16 * q < p.row_bytes;
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        a[i][r] = on && won[r] ? ldg_stream(wg[r] + k) : zero;
+        b[i][r] = on && won[r] ? ldg_stream(wu[r] + k) : zero;
+      }
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        x[i][n] = on && xon[n] ? __ldg(reinterpret_cast<const uint4*>(xp[n] + k)) : zero;
+    }
+#pragma unroll
+    for (int i = 0; i < UN; ++i)
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma_16x8<E4M3>(acc[r][n], a[i][r].x, b[i][r].x, a[i][r].y, b[i][r].y, x[i][n].x, x[i][n].y);
+          mma_16x8<E4M3>(acc[r][n], a[i][r].z, b[i][r].z, a[i][r].w, b[i][r].w, x[i][n].z, x[i][n].w);
+        }
+  }
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) red[warp][(r * NT + n) * 4 + i][lane] = acc[r][n][i];
+  __syncthreads();
+  // output (column c, token t): accumulator of tile (c / 8, t / 8), lane 4 (c % 8) + (t % 8) / 2, slot t % 2 (gate),
+  // 2 + t % 2 (up)
+  for (int o = threadIdx.x; o < kCols * kToks; o += 256) {
+    const int c = o % kCols, t = o / kCols, f = f0 + c;
+    if (f >= p.F || t >= p.N) continue;
+    const int slot = ((c >> 3) * NT + (t >> 3)) * 4 + (t & 1), l = 4 * (c & 7) + ((t & 7) >> 1);
+    float gate = 0.f, up = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      gate += red[w][slot][l];
+      up += red[w][slot + 2][l];
+    }
+    if (E4M3) {
+      const float xs = __ldg(p.xs + t);
+      gate *= xs * __ldg(p.gs + f);
+      up *= xs * __ldg(p.us + f);
+    }
+    p.out[(size_t)t * p.F + f] = __float2bfloat16_rn(act_of<ACT>(gate) * up);
+  }
+}
+
+template <bool E4M3, int ACT>
+static moga_status launch_few(const FewParams& p, const char* who, cudaStream_t s) {
+  if (p.N <= 8) ffn_few_kernel<E4M3, ACT, 1, 1, 8><<<ceil_div(p.F, 8), 256, 0, s>>>(p);
+  else if (p.N <= 16) ffn_few_kernel<E4M3, ACT, 2, 2, 4><<<ceil_div(p.F, 16), 256, 0, s>>>(p);
+  else ffn_few_kernel<E4M3, ACT, 2, 4, 4><<<ceil_div(p.F, 16), 256, 0, s>>>(p);
+  return check_launch(who);
+}
+
 // Row-major [rows][cols] matrix of 1- or 2-byte elements, boxes of 128 bytes x box_rows.
 static moga_status make_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols, int elem, int box_rows) {
   auto fn = route_tc::encode_fn();
@@ -417,6 +552,23 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
                        reinterpret_cast<uintptr_t>(w_up_scale);
   if ((a & 15) || (a4 & 3))
     return fail(MOGA_ERR_INVALID_ARG, "%s: x, w_gate, w_up, out must be 16-byte aligned", who);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (N <= kFewTokens) {
+    FewParams q = {};
+    q.x = static_cast<const uint8_t*>(x);
+    q.wg = static_cast<const uint8_t*>(w_gate);
+    q.wu = static_cast<const uint8_t*>(w_up);
+    q.N = (int)N;
+    q.F = F;
+    q.row_bytes = d * elem;
+    q.xs = x_scale;
+    q.gs = w_gate_scale;
+    q.us = w_up_scale;
+    q.out = static_cast<__nv_bfloat16*>(out);
+    if (act == MOGA_ACT_SILU)
+      return f8 ? launch_few<true, MOGA_ACT_SILU>(q, who, s) : launch_few<false, MOGA_ACT_SILU>(q, who, s);
+    return f8 ? launch_few<true, MOGA_ACT_GELU>(q, who, s) : launch_few<false, MOGA_ACT_GELU>(q, who, s);
+  }
   CUtensorMap mx, mg, mu;
   if ((st = make_map(&mx, x, N, d, elem, ffn::BM)) != MOGA_OK) return st;
   if ((st = make_map(&mg, w_gate, F, d, elem, ffn::BN / 2)) != MOGA_OK) return st;
@@ -434,7 +586,6 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
   p.us = w_up_scale;
   p.o0 = static_cast<__nv_bfloat16*>(out);
   p.timeout = kWaitLimitCycles;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
   return f8 ? launch_act<MODE_FWD, true>(p, mx, mg, mu, who, s) : launch_act<MODE_FWD, false>(p, mx, mg, mu, who, s);
 }
 
