@@ -49,6 +49,15 @@
  * out[7i .. 7i+6] = (head, query begin, query end, key begin, key end, tile
  * begin, tile end), the tile being a range of queries (keys = 0) or of keys
  * (keys = 1) of at most 128 rows.
+ *
+ * moga_test_ffn_units(grad, N, d, F, need_dx, need_dw, bn, sms, out, cap)
+ * returns the number n of work units of one launch of the gated feed-forward
+ * on `sms` SMs: with grad = 0 its tiles of bn accumulator columns, with
+ * grad = 1 the units of the gradient launch (dx tiles where need_dx, dW units
+ * where need_dw).  For unit i < min(n, cap), pair by pair in the order that
+ * the pair takes them, out[8i .. 8i+7] = (pair, kind (0 gated tile, 1 dx tile,
+ * 2 dW unit), up matrix, row tile, column tile, split, first k stage, end k
+ * stage).  Host code only.
  */
 #ifndef MOGA_TESTING_H
 #define MOGA_TESTING_H
@@ -67,6 +76,9 @@ int32_t moga_test_attn_tiles(int32_t mode, const int32_t* cu_seqlens, int32_t M,
 int32_t moga_test_window_tokens(const moga_stga_geom* geom, int32_t begin, int32_t end, int32_t* out);
 int32_t moga_test_bwd_units(int32_t mode, int32_t keys, const int32_t* cu_seqlens, int32_t M, int64_t N,
                             int32_t H, const moga_stga_geom* geom, int32_t* grid, int32_t* out, int32_t cap);
+
+int64_t moga_test_ffn_units(int32_t grad, int64_t N, int32_t d, int32_t F, int32_t need_dx, int32_t need_dw,
+                            int32_t bn, int32_t sms, int32_t* out, int64_t cap);
 
 #ifdef __cplusplus
 }

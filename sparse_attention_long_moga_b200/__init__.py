@@ -37,7 +37,8 @@ def _ptr(t):
 
 
 def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    # the current stream's handle without a torch.cuda.Stream object around it (3 us less per call)
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()))
 
 
 def _need(t, dtype, name, dim=None, shape=None, device=True):
@@ -59,14 +60,16 @@ def _need(t, dtype, name, dim=None, shape=None, device=True):
 
 def _on_device(**tensors):
     """Every tensor on the current CUDA device (the calls launch on its current stream)."""
+    cur = None
     for name, t in tensors.items():
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("%s must be a CUDA tensor" % name)
-        if t.device.index != torch.cuda.current_device():
-            raise ValueError("%s is on %s but the calls run on the current device cuda:%d"
-                             % (name, t.device, torch.cuda.current_device()))
+        if cur is None:
+            cur = torch.cuda.current_device()
+        if t.get_device() != cur:
+            raise ValueError("%s is on %s but the calls run on the current device cuda:%d" % (name, t.device, cur))
 
 
 def _check_geom(geom: dict, N: int):
@@ -533,8 +536,8 @@ def moga_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
     _on_device(x=x, weight=weight, residual=residual, h=h)
     if residual is not None and h is None:
         h = torch.empty_like(residual)
-    y = torch.empty((N, d), dtype=out_dtype, device=x.device)
-    scale = torch.empty(N, dtype=torch.float32, device=x.device) if out_dtype == torch.float8_e4m3fn else None
+    y = torch.empty_like(x, dtype=out_dtype)
+    scale = x.new_empty(N, dtype=torch.float32) if out_dtype == torch.float8_e4m3fn else None
     check(lib().moga_rms_norm(_ptr(x), x_dt, _ptr(residual), r_dt, _ptr(weight), w_dt, N, d, eps, _ptr(h), _ptr(y),
                               _NORM_DT[out_dtype], _ptr(scale), _stream()), "moga_rms_norm")
     return y, x if residual is None else h, scale
@@ -561,14 +564,13 @@ def moga_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
         raise ValueError("branch_dtype must be None or bfloat16, got %s" % branch_dtype)
     _on_device(dy=dy, h=h, weight=weight, dres=dres, dx=dx)
     L = lib()
-    dev = h.device
     if dx is None:
         dx = torch.empty_like(h)
-    dxb = torch.empty((N, d), dtype=torch.bfloat16, device=dev) if branch_dtype is not None else None
+    dxb = torch.empty_like(h, dtype=torch.bfloat16) if branch_dtype is not None else None
     dw = ws = None
     if need_dw:
-        dw = torch.empty(d, dtype=torch.float32, device=dev)
-        ws = torch.empty(max(L.moga_rms_norm_bwd_ws_bytes(N, d), 16), dtype=torch.uint8, device=dev)
+        dw = h.new_empty(d, dtype=torch.float32)
+        ws = h.new_empty(max(L.moga_rms_norm_bwd_ws_bytes(N, d), 16), dtype=torch.uint8)
     check(L.moga_rms_norm_bwd(_ptr(dy), dy_dt, _ptr(h), h_dt, _ptr(weight), w_dt, _ptr(dres), N, d, eps, _ptr(dx),
                               _ptr(dxb), _ptr(dw), _ptr(ws), ws.numel() if need_dw else 0, _stream()),
           "moga_rms_norm_bwd")
@@ -608,7 +610,7 @@ def moga_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ac
         else:
             _need(t, torch.float32, name, 1, (n,), device=False)
     _on_device(x=x, w_gate=w_gate, w_up=w_up, x_scale=x_scale, w_gate_scale=w_gate_scale, w_up_scale=w_up_scale)
-    out = torch.empty((N, F), dtype=torch.bfloat16, device=x.device)
+    out = x.new_empty((N, F), dtype=torch.bfloat16)
     check(lib().moga_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _NORM_DT[x.dtype], _ptr(x_scale),
                                _ptr(w_gate_scale), _ptr(w_up_scale), N, d, F, _ACTS[act], _ptr(out), _stream()),
           "moga_gated_ffn")
@@ -624,10 +626,9 @@ def moga_gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.T
     _need(dout, torch.bfloat16, "dout", 2, (N, F), device=False)
     _on_device(x=x, w_gate=w_gate, w_up=w_up, dout=dout)
     L = lib()
-    b16 = dict(dtype=torch.bfloat16, device=x.device)
-    dx = torch.empty((N, d), **b16) if need_dx else None
-    dwg, dwu = (torch.empty((F, d), **b16) if need_dw else None for _ in range(2))
-    ws = torch.empty(max(L.moga_gated_ffn_bwd_ws_bytes(N, d, F), 16), dtype=torch.uint8, device=x.device)
+    dx = torch.empty_like(x) if need_dx else None
+    dwg, dwu = (torch.empty_like(w_gate) if need_dw else None for _ in range(2))
+    ws = x.new_empty(max(L.moga_gated_ffn_bwd_ws_bytes(N, d, F), 16), dtype=torch.uint8)
     check(L.moga_gated_ffn_bwd(_ptr(x), _ptr(w_gate), _ptr(w_up), N, d, F, _ACTS[act], _ptr(dout), _ptr(dx),
                                _ptr(dwg), _ptr(dwu), _ptr(ws), ws.numel(), _stream()), "moga_gated_ffn_bwd")
     return dict(dx=dx, dw_gate=dwg, dw_up=dwu)

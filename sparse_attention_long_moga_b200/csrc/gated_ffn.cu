@@ -2,27 +2,30 @@
 // SMs (clusters of two CTAs, cta_group::2).
 //
 // Forward:   o = act(g) * u,   g = x Wg^T,  u = x Wu^T      (x [N][d], Wg, Wu [F][d])
-//   one kernel: a tile is 256 tokens x 128 columns of F.  The leader CTA's B
-//   rows are 128 rows of Wg, its peer's the same 128 rows of Wu, so the
-//   256-column product of the pair holds a token's gate in columns [0, 128)
-//   and its up value in [128, 256) of the same TMEM lane, and the epilogue
+//   one kernel: a tile is 256 tokens x BN / 2 columns of F.  The leader CTA's
+//   B rows are BN / 2 rows of Wg, its peer's the same rows of Wu, so the
+//   BN-column product of the pair holds a token's gate in columns [0, BN / 2)
+//   and its up value in [BN / 2, BN) of the same TMEM lane, and the epilogue
 //   forms act(g) * u from fp32 accumulators without g or u ever leaving the SM.
 //   e4m3 operands (kind::f8f6f4) keep the tile in bytes: 128 k a stage instead
 //   of 64; the scales (one per token, one per weight row) are factors of the
 //   accumulators, applied in fp32 in the epilogue.
 // Backward, given do = dL/do:
 //   dg = do * u * act'(g), du = do * act(g)      g, u computed again by the forward's product
-//   dx = dg Wg + du Wu                           one product, K = 2F
-//   dWg = dg^T x, dWu = du^T x                   one launch, K = N
+//   dx = dg Wg + du Wu                           K = 2F
+//   dWg = dg^T x, dWu = du^T x                   K = N
 //   g and u are recomputed (4 N d F of the 12 N d F operations) instead of
 //   saved: a saved pair would hold 4 N F bytes per layer from the forward to
 //   the backward and would be rounded to bf16.  dg and du are rounded to bf16
 //   (the tensor core's operand type) once and live in the workspace only.
+//   dx and dW share one launch (see "gradient units"), of 512-row tiles where
+//   there are enough of them.
 //
-// 192 threads per CTA: warp 4 TMA producer, warp 5 TMEM allocator and (leader)
-// MMA issuer, warps 0-3 epilogue, thread = token row = TMEM lane.  Two
-// 256-column accumulators let a tile's epilogue overlap the next tile's
-// products.  All waits are bounded.
+// 320 threads per CTA: warps 0-7 epilogue (thread = TMEM lane of its warp's
+// quarter, two warps per quarter with half of the columns each), warp 8 TMA
+// producer, warp 9 TMEM allocator and (leader) MMA issuer.  Two accumulators
+// of BN columns let a tile's epilogue overlap the next tile's products.  All
+// waits are bounded.
 #include "common.cuh"
 #include "tc_common.cuh"
 
@@ -31,50 +34,107 @@ namespace ffn {
 
 using namespace moga::tc;
 
-enum Mode { MODE_FWD = 0, MODE_DGDU = 1, MODE_DX = 2, MODE_DW = 3 };
+enum Mode { MODE_FWD = 0, MODE_DGDU = 1, MODE_GRAD = 2 };
 
 constexpr int BM = 128;                      // accumulator rows per CTA (256 per pair)
-constexpr int BN = 256;                      // accumulator columns of a tile
-constexpr int kStages = 6;
-constexpr int kThreads = 192;
 constexpr int kRowBytes = 128;               // bytes of one operand row in a stage (one swizzle span)
-constexpr int kOpBytes = 128 * kRowBytes;    // 16 KB: one operand of one CTA in a stage
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kBarOff = kStages * kStageBytes;
-constexpr int kMiscOff = kBarOff + 32 * 8;
-constexpr int kSmemBytes = kMiscOff + 64 + 1024;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory");
+constexpr int kHalfBox = 64 * kRowBytes;     // 8 KB: a box of 64 rows
+constexpr int kOutBox = 32 * kRowBytes;      // 4 KB: a warp's 32 rows x 64 bf16 columns of output
 constexpr int kGroupM = 8;                   // row tiles per band of the tile order
 
-constexpr int B_FULL = 0;                    // [kStages]
-constexpr int B_EMPTY = kStages;             // [kStages]
-constexpr int B_ACC_FULL = 2 * kStages;      // [2]
-constexpr int B_ACC_EMPTY = B_ACC_FULL + 2;  // [2] (both CTAs' epilogue threads)
-constexpr int B_END = B_ACC_EMPTY + 2;
-static_assert(B_END < 32, "barrier area");
+// Accumulators: HM = 1: 256 rows per pair, two buffers of BN columns;
+// HM = 2: 512 rows, the two accumulators hold a CTA's two halves of 128 rows.
+template <int BN, int HM>
+struct Tile {
+  static constexpr int kABytes = HM * BM * kRowBytes;     // this CTA's rows of A
+  static constexpr int kBBytes = BN / 2 * kRowBytes;      // this CTA's half of the B rows
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kStages = HM == 2 ? 4 : BN == 256 ? 6 : 8;
+  static constexpr int kOutOff = kStages * kStageBytes;   // output boxes of the epilogue warps
+  static constexpr int kBarOff = kOutOff + 8 * kOutBox;
+  static constexpr int kMiscOff = kBarOff + 32 * 8;
+  static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
+  static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2,
+                       kEnd = kAccEmpty + 2;
+  static_assert(kSmemBytes <= 227 * 1024 && kEnd < 32, "shared memory");
+};
 
 struct Params {
-  int rows, cols;            // of the output (FWD, DGDU: N x F; DX: N x d; DW: F x d)
-  int n_k;                   // k stages of a tile
-  int seg_k;                 // DX: stages of the gate half (F / 64 rounded up)
-  int m_tiles, n_tiles;      // 256-row tiles (DW: of one matrix), column tiles
-  int total;                 // tiles
+  int rows, cols;            // FWD, DGDU: N, F;  GRAD: N, d
+  int n_k;                   // k stages of a forward tile
+  int m_tiles, n_tiles;      // row tiles of N (256 HM rows), column tiles of F (FWD, DGDU) or d (GRAD)
+  int a_box;                 // FWD, DGDU: rows of a box of x
+  int total;                 // FWD, DGDU: tiles
   int act;
   const float *xs, *gs, *us; // e4m3 scales
   const __nv_bfloat16* dh;   // DGDU
-  __nv_bfloat16 *o0, *o1;    // FWD: o; DGDU: dg, du; DX: dx; DW: dWg, dWu
+  // GRAD
+  float* partial;            // [splits][2][F][d] where K is split, else NULL
+  int F;
+  int seg_k;                 // stages of the gate half of dx's K (F / 64 rounded up)
+  int mf_tiles;              // row tiles of F
+  int n_dw, kc, kdw;         // dW units (tiles x splits), stages of one, stages of N
+  int n_dx;                  // dx tiles
+  int n1, a, b;              // dx tiles of the first n1 pairs (one dW unit more), of the others
   long long timeout;
+};
+
+// One piece of work of a pair: rows and columns of a tile, its k stages.
+struct Unit {
+  int kind;                  // 0: gated tile, 1: dx tile, 2: dW tile
+  int m, n, k0, k1, split, up;
 };
 
 // Tile t -> (row tile, column tile).  Tiles run down bands of kGroupM row
 // tiles, so that the pairs at work at one time share a few row tiles and a
 // few column tiles in L2 instead of sweeping all of W for every row tile.
-__device__ __forceinline__ void tile_of(int t, int m_tiles, int n_tiles, int* m, int* n) {
+__host__ __device__ __forceinline__ void tile_of(int t, int m_tiles, int n_tiles, int* m, int* n) {
   const int band = kGroupM * n_tiles;
   const int b = t / band, r = t - b * band;
-  const int gm = min(kGroupM, m_tiles - b * kGroupM);
+  const int gm = m_tiles - b * kGroupM < kGroupM ? m_tiles - b * kGroupM : kGroupM;
   *n = r / gm;
   *m = b * kGroupM + (r - *n * gm);
+}
+
+// Gradient units.  dW tiles are few and long (K = N), dx tiles many and short
+// (K = 2F), and neither count fills the pairs' last round; together they do.
+// Each pair takes its dW units first (unit j P + pair), then dx tiles: the n1
+// pairs that have one dW unit more take `a` of them, the others `b`, with
+// b - a dx tiles about as long as a dW unit (plan_grad).
+// The j-th unit of pair `pair` of `P`; false when it has no more.
+template <int MODE>
+__host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int P, int j, Unit* u) {
+  u->split = u->up = 0;
+  if (MODE != MODE_GRAD) {
+    const int t = j * P + pair;   // total < 2^30, P < 2^10: no overflow where the loop stops at the first false
+    if (t >= p.total) return false;
+    u->kind = 0;
+    u->k0 = 0;
+    u->k1 = p.n_k;
+    tile_of(t, p.m_tiles, p.n_tiles, &u->m, &u->n);
+    return true;
+  }
+  const int mine = p.n_dw / P + (pair < p.n_dw % P ? 1 : 0);
+  if (j < mine) {
+    const int t = j * P + pair, tiles = 2 * p.mf_tiles * p.n_tiles;
+    u->kind = 2;
+    u->split = t / tiles;
+    tile_of(t - u->split * tiles, 2 * p.mf_tiles, p.n_tiles, &u->m, &u->n);
+    u->up = u->m >= p.mf_tiles;
+    if (u->up) u->m -= p.mf_tiles;
+    u->k0 = u->split * p.kc;
+    u->k1 = u->k0 + p.kc < p.kdw ? u->k0 + p.kc : p.kdw;
+    return true;
+  }
+  const int i = j - mine;
+  if (i >= (pair < p.n1 ? p.a : p.b)) return false;
+  const int t = i < p.a || p.n1 == 0 ? i * P + pair : p.a * P + (i - p.a) * (P - p.n1) + pair - p.n1;
+  if (t >= p.n_dx) return false;
+  u->kind = 1;
+  u->k0 = 0;
+  u->k1 = 2 * p.seg_k;
+  tile_of(t, p.m_tiles, p.n_tiles, &u->m, &u->n);
+  return true;
 }
 
 __device__ __forceinline__ void mma_pair_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
@@ -85,12 +145,6 @@ __device__ __forceinline__ void mma_pair_f8(uint32_t d_tmem, uint64_t adesc, uin
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-
-// instruction descriptors of a pair's M = 256, N = 256 product
-constexpr uint32_t kIdescBf16 = pair_desc(instr_desc(BN, false));
-constexpr uint32_t kIdescBMn = pair_desc(instr_desc(BN, true));
-constexpr uint32_t kIdescABMn = kIdescBMn | (1u << 15);
-constexpr uint32_t kIdescE4m3 = kIdescBf16 & ~((7u << 7) | (7u << 10));   // e4m3 x e4m3 (format 0)
 
 // Activation and its derivative in fp32.  silu: g s, s = 1 / (1 + e^-g);
 // gelu: the tanh form, 0.5 (1 + tanh z) = 1 / (1 + e^-2z),
@@ -121,76 +175,197 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// 32 fp32 values to bf16 columns [col, col + 32) of a row; columns at or past
-// `cols` (a multiple of 8) are skipped
-__device__ __forceinline__ void store32(__nv_bfloat16* row, int col, int cols, const float* v) {
+// ---- output boxes.  A thread owns a row, so its own 16-byte stores would
+// touch 32 lines per warp instruction and half a sector each.  Instead a warp
+// lays 32 rows x 64 columns of bf16 into shared memory (128-byte rows, the
+// TMA's 128-byte swizzle: conflict-free for row-owning lanes) and one lane
+// stores the box through the tensor map, which writes whole lines and clips
+// rows and columns past the tensor's end.
+__device__ __forceinline__ uint32_t box_addr(uint32_t box, int row, int piece) {
+  return box + row * kRowBytes + ((piece ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+// 32 values of the lane's row into pieces [4 half, 4 half + 4) of a box
+__device__ __forceinline__ void put32(uint32_t box, int lane, int half, const float* v) {
 #pragma unroll
   for (int e = 0; e < 4; ++e)
-    if (col + 8 * e < cols)
-      *reinterpret_cast<uint4*>(row + col + 8 * e) =
+    sts16(box_addr(box, lane, 4 * half + e),
           make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]),
-                     pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7]));
+                     pack2(v[8 * e + 4], v[8 * e + 5]), pack2(v[8 * e + 6], v[8 * e + 7])));
+}
+// the warp's writes to the box become visible to the TMA, then one lane stores it
+__device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t box, int col, int row, int lane) {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  __syncwarp();
+  if (lane == 0) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(col), "r"(row), "r"(box)
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+}
+// the box of all but the last PENDING stores may be written again
+template <int PENDING>
+__device__ __forceinline__ void boxes_free(int lane) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(PENDING) : "memory");
+  __syncwarp();
 }
 
-template <int MODE, bool E4M3, int ACT>
-__device__ __forceinline__ void epilogue_gated(const Params& p, uint32_t acc, int row, int col0) {
-  const bool in = row < p.rows;
-  const float xs = E4M3 && in ? __ldg(p.xs + row) : 1.f;
+// A gated tile's BN / 2 columns for the warp's 32 rows from row0.  `turn`
+// counts the warp's stores: its two boxes are filled in turn.
+template <bool E4M3, int ACT, int BN>
+__device__ __forceinline__ void epilogue_fwd(const Params& p, const CUtensorMap* map, uint32_t acc, uint32_t boxes,
+                                             int row0, int col0, int lane, int& turn) {
+  const int row = row0 + lane;
+  const float xs = E4M3 && row < p.rows ? __ldg(p.xs + row) : 1.f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < BN / 2; c0 += 32) {
-    float g[32], u[32];
-    tmem_ld32(acc + c0, g);
-    tmem_ld32(acc + BN / 2 + c0, u);
-    tmem_wait_ld();
+  for (int c0 = 0; c0 < BN / 2; c0 += 64) {
     const int col = col0 + c0;
-    if (in && col < p.cols) {
+    if (col >= p.cols || row0 >= p.rows) break;   // the whole warp
+    const uint32_t box = boxes + (turn++ & 1) * kOutBox;
+    boxes_free<1>(lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float g[32], u[32];
+      tmem_ld32(acc + c0 + 32 * h, g);
+      tmem_ld32(acc + BN / 2 + c0 + 32 * h, u);
+      tmem_wait_ld();
       if (E4M3) {
 #pragma unroll
         for (int j = 0; j < 32; ++j) {
-          const int cc = min(col + j, p.cols - 1);
+          const int cc = min(col + 32 * h + j, p.cols - 1);
           g[j] *= xs * __ldg(p.gs + cc);
           u[j] *= xs * __ldg(p.us + cc);
         }
       }
-      if (MODE == MODE_FWD) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) g[j] = act_of<ACT>(g[j]) * u[j];
-        store32(p.o0 + (size_t)row * p.cols, col, p.cols, g);
-      } else {
-        const __nv_bfloat16* dh = p.dh + (size_t)row * p.cols + col;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          uint4 t = make_uint4(0, 0, 0, 0);
-          if (col + 8 * e < p.cols) t = *reinterpret_cast<const uint4*>(dh + 8 * e);
-          const uint32_t w[4] = {t.x, t.y, t.z, t.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float d = __uint_as_float((i & 1) ? (w[i >> 1] & 0xffff0000u) : (w[i >> 1] << 16));
-            float a, da;
-            act_and_grad<ACT>(g[8 * e + i], &a, &da);
-            g[8 * e + i] = d * u[8 * e + i] * da;
-            u[8 * e + i] = d * a;
-          }
-        }
-        store32(p.o0 + (size_t)row * p.cols, col, p.cols, g);
-        store32(p.o1 + (size_t)row * p.cols, col, p.cols, u);
-      }
+      for (int j = 0; j < 32; ++j) g[j] = act_of<ACT>(g[j]) * u[j];
+      put32(box, lane, h, g);
     }
-    __syncwarp();   // the next tcgen05.ld is the whole warp's
+    store_box(map, box, col, row0, lane);
   }
 }
 
-template <int MODE, bool E4M3, int ACT>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
-ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap tm_a0,
-           const __grid_constant__ CUtensorMap tm_a1, const __grid_constant__ CUtensorMap tm_b0,
-           const __grid_constant__ CUtensorMap tm_b1) {
+// The warp's 32 rows x 64 columns of dout, 8 lanes a row (whole lines).
+__device__ __forceinline__ void load_dout(const Params& p, int row0, int col, int lane, uint4* v) {
+  const int c = col + 8 * (lane & 7);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = row0 + 4 * i + (lane >> 3);
+    v[i] = r < p.rows && c < p.cols ? __ldg(reinterpret_cast<const uint4*>(p.dh + (size_t)r * p.cols + c))
+                                    : make_uint4(0, 0, 0, 0);
+  }
+}
+
+// dg and du of a gated tile's BN / 2 columns; v holds the first 64 columns of
+// dout (loaded before the products were waited for).
+template <int ACT, int BN>
+__device__ __forceinline__ void epilogue_dgdu(const Params& p, const CUtensorMap* mg, const CUtensorMap* mu,
+                                              uint32_t acc, uint32_t boxes, int row0, int col0, int lane, uint4* v) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < BN / 2; c0 += 64) {
+    const int col = col0 + c0;
+    if (col >= p.cols || row0 >= p.rows) break;   // the whole warp
+    if (c0 > 0) load_dout(p, row0, col, lane, v);
+    boxes_free<0>(lane);
+    // dout from lanes of columns to lanes of rows, through the first box
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sts16(box_addr(boxes, 4 * i + (lane >> 3), lane & 7), v[i]);
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t w[16];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint4 t = lds16(box_addr(boxes, lane, 4 * h + e));
+        w[4 * e] = t.x; w[4 * e + 1] = t.y; w[4 * e + 2] = t.z; w[4 * e + 3] = t.w;
+      }
+      float g[32], u[32];
+      tmem_ld32(acc + c0 + 32 * h, g);
+      tmem_ld32(acc + BN / 2 + c0 + 32 * h, u);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) {
+        const float d = __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
+        float a, da;
+        act_and_grad<ACT>(g[j], &a, &da);
+        g[j] = d * u[j] * da;
+        u[j] = d * a;
+      }
+      put32(boxes, lane, h, g);            // the lane's own row and half, read above
+      put32(boxes + kOutBox, lane, h, u);
+    }
+    store_box(mg, boxes, col, row0, lane);
+    store_box(mu, boxes + kOutBox, col, row0, lane);
+  }
+}
+
+// Columns [c_begin, c_begin + COLS) of a gradient tile for the warp's 32 rows:
+// bf16 through the box, or the fp32 partial sum where K is split.
+template <int BN, int COLS>
+__device__ __forceinline__ void epilogue_grad(const Params& p, const CUtensorMap* map, const Unit& u, uint32_t acc,
+                                              uint32_t box, int row0, int c_begin, int lane) {
+  const int rows = u.kind == 1 ? p.rows : p.F;
+#pragma unroll 1
+  for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 64) {
+    const int col = u.n * BN + c0;
+    if (col >= p.cols || row0 >= rows) break;   // the whole warp
+    const bool split = u.kind == 2 && p.partial;
+    if (!split) boxes_free<0>(lane);
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      float v[32];
+      tmem_ld32(acc + c0 + 32 * h, v);
+      tmem_wait_ld();
+      if (!split) {
+        put32(box, lane, h, v);
+      } else if (row0 + lane < rows) {
+        float* dst = p.partial + ((size_t)(u.split * 2 + u.up) * p.F + row0 + lane) * p.cols + col + 32 * h;
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (col + 32 * h + 4 * e < p.cols)
+            *reinterpret_cast<float4*>(dst + 4 * e) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+      }
+      __syncwarp();
+    }
+    if (!split) store_box(map, box, col, row0, lane);
+  }
+}
+
+// Tensor maps.  Loads: FWD, DGDU: 0 x (a_box-row boxes), 1 w_gate, 2 w_up
+// (BN / 2-row boxes); GRAD: 0 x, 1 w_gate, 2 w_up, 3 dg, 4 du (64 x 64 boxes).
+// Stores (32-row boxes): FWD: out; DGDU: dg, du; GRAD: dx, dw_gate, dw_up.
+struct Maps {
+  CUtensorMap m[5], out[3];
+};
+
+template <int MODE, bool E4M3, int ACT, int BN, int HM, int EW>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((EW + 2) * 32, 1)
+ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
+  using T = Tile<BN, HM>;
   constexpr int BK = E4M3 ? 128 : 64;
+  // instruction descriptors of a pair's M = 256 product
+  constexpr uint32_t kIdesc = pair_desc(instr_desc(BN, false));
+  constexpr uint32_t kIdescBMn = pair_desc(instr_desc(BN, true));
+  constexpr uint32_t kIdescABMn = kIdescBMn | (1u << 15);
+  constexpr uint32_t kIdescE4m3 = kIdesc & ~((7u << 7) | (7u << 10));   // e4m3 x e4m3 (format 0)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const uint32_t sbase = smem_u32(smem);
-  auto bar = [&](int i) { return sbase + kBarOff + 8u * (uint32_t)i; };
-  int* misc = reinterpret_cast<int*>(smem + kMiscOff);
+  auto bar = [&](int i) { return sbase + T::kBarOff + 8u * (uint32_t)i; };
+  int* misc = reinterpret_cast<int*>(smem + T::kMiscOff);
   volatile int* abort_flag = misc;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(misc + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -200,20 +375,20 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(bar(B_FULL + s), 1);
-      mbar_init(bar(B_EMPTY + s), 1);
+    for (int s = 0; s < T::kStages; ++s) {
+      mbar_init(bar(T::kFull + s), 1);
+      mbar_init(bar(T::kEmpty + s), 1);
     }
     for (int b = 0; b < 2; ++b) {
-      mbar_init(bar(B_ACC_FULL + b), 1);
-      mbar_init(bar(B_ACC_EMPTY + b), 2 * BM);
+      mbar_init(bar(T::kAccFull + b), 1);
+      mbar_init(bar(T::kAccEmpty + b), 2 * EW);   // a warp's arrival stands for its lanes
     }
-    mbar_init(bar(B_END), 1);
+    mbar_init(bar(T::kEnd), 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == EW + 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)),
-                 "r"(512u)
+                 "r"(2u * BN)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
   }
@@ -222,117 +397,143 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap
   cluster_sync();   // both CTAs' barriers are initialised before any remote use
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-  // row tile (of both matrices in DW) and column tile of tile t
-  auto decode = [&](int t, int* m, int* n) {
-    tile_of(t, MODE == MODE_DW ? 2 * p.m_tiles : p.m_tiles, p.n_tiles, m, n);
-  };
 
-  if (warp == 4) {
+  if (warp == EW) {
     // ------------------------------------------------------------------ producer
     if (lane == 0) {
       int c = 0;
       bool ok = true;
-      for (int t = pair; t < p.total && ok; t += n_pairs) {
-        int m, n;
-        decode(t, &m, &n);
-        for (int kt = 0; kt < p.n_k; ++kt, ++c) {
-          const int st = c % kStages;
-          if (!(ok = mbar_wait(bar(B_EMPTY + st), ((c / kStages) & 1) ^ 1, abort_flag, p.timeout))) break;
-          const uint32_t full = peer_addr(bar(B_FULL + st), 0);
+      Unit u;
+      for (int j = 0; ok && unit_of<MODE>(p, pair, n_pairs, j, &u); ++j) {
+        for (int kt = u.k0; kt < u.k1; ++kt, ++c) {
+          const int st = c % T::kStages;
+          if (!(ok = mbar_wait(bar(T::kEmpty + st), ((c / T::kStages) & 1) ^ 1, abort_flag, p.timeout))) break;
+          const uint32_t full = peer_addr(bar(T::kFull + st), 0);
+          // Rows of A past the last token are left unloaded (their products
+          // reach no output): the peer's tile where it has no row, and all
+          // but a_box rows of the leader's where there are fewer tokens.
+          const bool peer_a = MODE == MODE_GRAD || (u.m * 2 + 1) * BM < p.rows;
           // the leader's barrier expects both CTAs' bytes
-          if (leader) mbar_arrive_expect_tx(bar(B_FULL + st), 2 * kStageBytes);
-          const uint32_t a = sbase + st * kStageBytes, b = a + kOpBytes;
-          if (MODE == MODE_FWD || MODE == MODE_DGDU) {
-            tma_load_2d_pair(a, &tm_a0, kt * BK, (m * 2 + (int)rank) * BM, full);
-            tma_load_2d_pair(b, leader ? &tm_b0 : &tm_b1, kt * BK, n * (BN / 2), full);
-          } else if (MODE == MODE_DX) {
-            const bool up = kt >= p.seg_k;
-            const int k0 = (up ? kt - p.seg_k : kt) * BK;
-            const CUtensorMap* mb = up ? &tm_b1 : &tm_b0;
-            const int c0 = n * BN + (int)rank * (BN / 2);
-            tma_load_2d_pair(a, up ? &tm_a1 : &tm_a0, k0, (m * 2 + (int)rank) * BM, full);
-            tma_load_2d_pair(b, mb, c0, k0, full);                       // 64 columns x 64 k rows
-            tma_load_2d_pair(b + kOpBytes / 2, mb, c0 + 64, k0, full);
+          if (leader) {
+            const int a_bytes = MODE == MODE_GRAD ? 2 * T::kABytes : (peer_a ? 2 : 1) * p.a_box * kRowBytes;
+            mbar_arrive_expect_tx(bar(T::kFull + st), a_bytes + 2 * T::kBBytes);
+          }
+          const uint32_t a = sbase + st * T::kStageBytes, b = a + T::kABytes;
+          if (MODE != MODE_GRAD) {
+            if (leader || peer_a) tma_load_2d_pair(a, &maps.m[0], kt * BK, (u.m * 2 + (int)rank) * BM, full);
+            tma_load_2d_pair(b, leader ? &maps.m[1] : &maps.m[2], kt * BK, u.n * (BN / 2), full);
           } else {
-            const bool up = m >= p.m_tiles;
-            const CUtensorMap* ma = up ? &tm_a1 : &tm_a0;
-            const int r0 = ((up ? m - p.m_tiles : m) * 2 + (int)rank) * BM;
-            const int c0 = n * BN + (int)rank * (BN / 2);
-            tma_load_2d_pair(a, ma, r0, kt * BK, full);
-            tma_load_2d_pair(a + kOpBytes / 2, ma, r0 + 64, kt * BK, full);
-            tma_load_2d_pair(b, &tm_b0, c0, kt * BK, full);
-            tma_load_2d_pair(b + kOpBytes / 2, &tm_b0, c0 + 64, kt * BK, full);
+            // this CTA's rows of A, and its half of the tile's columns, in boxes of 64
+            const int r0 = (u.m * 2 + (int)rank) * HM * BM, c0 = u.n * BN + (int)rank * (BN / 2);
+            if (u.kind == 1) {
+              const bool up = kt >= p.seg_k;
+              const int k0 = (up ? kt - p.seg_k : kt) * BK;
+              const CUtensorMap *ma = up ? &maps.m[4] : &maps.m[3], *mb = up ? &maps.m[2] : &maps.m[1];
+#pragma unroll
+              for (int i = 0; i < 2 * HM; ++i) tma_load_2d_pair(a + i * kHalfBox, ma, k0, r0 + 64 * i, full);
+              tma_load_2d_pair(b, mb, c0, k0, full);
+              tma_load_2d_pair(b + kHalfBox, mb, c0 + 64, k0, full);
+            } else {
+              const CUtensorMap* ma = u.up ? &maps.m[4] : &maps.m[3];
+#pragma unroll
+              for (int i = 0; i < 2 * HM; ++i) tma_load_2d_pair(a + i * kHalfBox, ma, r0 + 64 * i, kt * BK, full);
+              tma_load_2d_pair(b, &maps.m[0], c0, kt * BK, full);
+              tma_load_2d_pair(b + kHalfBox, &maps.m[0], c0 + 64, kt * BK, full);
+            }
           }
         }
       }
     }
     __syncwarp();
-  } else if (warp == 5) {
+  } else if (warp == EW + 1) {
     // ------------------------------------------------------------------ MMA issuer (leader)
     if (leader && lane == 0) {
-      int c = 0, j = 0;   // stage and local tile counters
+      int c = 0;   // stage counter
       bool ok = true;
-      for (int t = pair; t < p.total && ok; t += n_pairs, ++j) {
-        const int b = j & 1;
-        if (!(ok = mbar_wait(bar(B_ACC_EMPTY + b), ((j >> 1) & 1) ^ 1, abort_flag, p.timeout))) break;
+      Unit u;
+      for (int j = 0; ok && unit_of<MODE>(p, pair, n_pairs, j, &u); ++j) {
+        // HM = 1: tile j's buffer j & 1; HM = 2: both, taken one after the other
+        const int b = HM == 1 ? j & 1 : 0;
+        const uint32_t empty_parity = (HM == 1 ? (j >> 1) & 1 : j & 1) ^ 1;
+        if (!(ok = mbar_wait(bar(T::kAccEmpty + b), empty_parity, abort_flag, p.timeout))) break;
         tc_fence_after();
-        const uint32_t acc = tmem + b * BN;
-        for (int kt = 0; kt < p.n_k; ++kt, ++c) {
-          const int st = c % kStages;
-          if (!(ok = mbar_wait(bar(B_FULL + st), (c / kStages) & 1, abort_flag, p.timeout))) break;
+        for (int kt = u.k0; kt < u.k1; ++kt, ++c) {
+          const int st = c % T::kStages;
+          if (!(ok = mbar_wait(bar(T::kFull + st), (c / T::kStages) & 1, abort_flag, p.timeout))) break;
           tc_fence_after();
-          const uint32_t sa = sbase + st * kStageBytes, sb = sa + kOpBytes;
+          const uint32_t sb = sbase + st * T::kStageBytes + T::kABytes;
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks) {
-            const uint32_t accum = (kt > 0 || ks > 0) ? 1u : 0u;
-            // K-major operands advance 32 bytes along their rows; MN-major
-            // ones 16 k rows of 128 bytes (64-column halves kOpBytes / 2 apart)
-            const uint64_t ak = smem_desc(sa + ks * 32, 16, 1024), bk = smem_desc(sb + ks * 32, 16, 1024);
-            const uint64_t am = smem_desc(sa + ks * 2048, kOpBytes / 2, 1024);
-            const uint64_t bm = smem_desc(sb + ks * 2048, kOpBytes / 2, 1024);
-            if (MODE == MODE_DW) mma_pair(acc, am, bm, kIdescABMn, accum);
-            else if (MODE == MODE_DX) mma_pair(acc, ak, bm, kIdescBMn, accum);
-            else if (E4M3) mma_pair_f8(acc, ak, bk, kIdescE4m3, accum);
-            else mma_pair(acc, ak, bk, kIdescBf16, accum);
+          for (int h = 0; h < HM; ++h) {
+            if (h == 1 && kt == u.k0) {
+              if (!(ok = mbar_wait(bar(T::kAccEmpty + 1), empty_parity, abort_flag, p.timeout))) break;
+              tc_fence_after();
+            }
+            const uint32_t acc = tmem + (HM == 1 ? b : h) * BN;
+            const uint32_t sa = sbase + st * T::kStageBytes + h * BM * kRowBytes;
+            // K-major operands advance 32 bytes along their rows; MN-major ones
+            // 16 k rows of 128 bytes (their 64-column boxes are kHalfBox apart)
+            if (MODE != MODE_GRAD) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks) {
+                const uint64_t ad = smem_desc(sa + ks * 32, 16, 1024), bd = smem_desc(sb + ks * 32, 16, 1024);
+                const uint32_t accum = (kt > u.k0 || ks > 0) ? 1u : 0u;
+                if (E4M3) mma_pair_f8(acc, ad, bd, kIdescE4m3, accum);
+                else mma_pair(acc, ad, bd, kIdesc, accum);
+              }
+            } else if (u.kind == 1) {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_pair(acc, smem_desc(sa + ks * 32, 16, 1024), smem_desc(sb + ks * 2048, kHalfBox, 1024), kIdescBMn,
+                         (kt > u.k0 || ks > 0) ? 1u : 0u);
+            } else {
+#pragma unroll
+              for (int ks = 0; ks < 4; ++ks)
+                mma_pair(acc, smem_desc(sa + ks * 2048, kHalfBox, 1024), smem_desc(sb + ks * 2048, kHalfBox, 1024),
+                         kIdescABMn, (kt > u.k0 || ks > 0) ? 1u : 0u);
+            }
           }
-          commit_pair(bar(B_EMPTY + st));
+          if (!ok) break;
+          commit_pair(bar(T::kEmpty + st));
         }
         if (!ok) break;
-        commit_pair(bar(B_ACC_FULL + b));
+        commit_pair(bar(T::kAccFull + b));
       }
-      commit_pair(bar(B_END));
-      mbar_drain(bar(B_END), 0, p.timeout);
+      commit_pair(bar(T::kEnd));
+      mbar_drain(bar(T::kEnd), 0, p.timeout);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ epilogue
-    const uint32_t lane_addr = (uint32_t)(warp * 32) << 16;
-    int j = 0;
-    for (int t = pair; t < p.total; t += n_pairs, ++j) {
-      int m, n;
-      decode(t, &m, &n);
-      const int b = j & 1;
-      if (!__all_sync(0xffffffffu, mbar_wait(bar(B_ACC_FULL + b), (j >> 1) & 1, abort_flag, p.timeout))) break;
+    const int quarter = warp & 3, half = warp >> 2;
+    const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+    const uint32_t boxes = sbase + T::kOutOff + warp * (8 / EW) * kOutBox;   // this warp's boxes
+    int turn = 0;
+    Unit u;
+    for (int j = 0; unit_of<MODE>(p, pair, n_pairs, j, &u); ++j) {
+      const int b = HM == 1 ? j & 1 : 0;
+      const uint32_t parity = HM == 1 ? (j >> 1) & 1 : j & 1;
+      const int row0 = (u.m * 2 + (int)rank) * HM * BM + quarter * 32;
+      uint4 v[MODE == MODE_DGDU ? 8 : 1];
+      if (MODE == MODE_DGDU) load_dout(p, row0, u.n * (BN / 2), lane, v);
+      if (!__all_sync(0xffffffffu, mbar_wait(bar(T::kAccFull + b), parity, abort_flag, p.timeout))) break;
       tc_fence_after();
-      const uint32_t acc = tmem + lane_addr + b * BN;
-      if (MODE == MODE_FWD || MODE == MODE_DGDU) {
-        epilogue_gated<MODE, E4M3, ACT>(p, acc, (m * 2 + (int)rank) * BM + warp * 32 + lane, n * (BN / 2));
-      } else {
-        const bool up = MODE == MODE_DW && m >= p.m_tiles;
-        const int row = ((up ? m - p.m_tiles : m) * 2 + (int)rank) * BM + warp * 32 + lane;
-        __nv_bfloat16* out = (up ? p.o1 : p.o0) + (size_t)row * p.cols;
 #pragma unroll 1
-        for (int c0 = 0; c0 < BN; c0 += 32) {
-          float v[32];
-          tmem_ld32(acc + c0, v);
-          tmem_wait_ld();
-          if (row < p.rows) store32(out, n * BN + c0, p.cols, v);
-          __syncwarp();
-        }
+      for (int h = 0; h < HM; ++h) {
+        const uint32_t acc = tmem + lane_addr + (HM == 1 ? b : h) * BN;
+        if constexpr (MODE == MODE_FWD)
+          epilogue_fwd<E4M3, ACT, BN>(p, &maps.out[0], acc, boxes, row0, u.n * (BN / 2), lane, turn);
+        else if constexpr (MODE == MODE_DGDU)
+          epilogue_dgdu<ACT, BN>(p, &maps.out[0], &maps.out[1], acc, boxes, row0, u.n * (BN / 2), lane, v);
+        else
+          epilogue_grad<BN, BN * 4 / EW>(p, &maps.out[u.kind == 1 ? 0 : 1 + u.up], u, acc, boxes, row0 + h * BM,
+                                         half * (BN * 4 / EW), lane);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(peer_addr(bar(T::kAccEmpty + (HM == 1 ? b : h)), 0));
       }
-      tc_fence_before();
-      mbar_arrive_cluster(peer_addr(bar(B_ACC_EMPTY + b), 0));
     }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
 
   // every product of the pair has completed (the leader drained them) and no
@@ -341,7 +542,26 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap
   __syncthreads();
   cluster_sync();
   tc_fence_after();
-  if (warp == 5) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u) : "memory");
+  if (warp == EW + 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * BN) : "memory");
+}
+
+// dW = bf16 of the sum of the K splits' partial sums, in split order;
+// n8 = F d / 8 groups of 8 values per matrix.
+__global__ void __launch_bounds__(256) ffn_dw_sum_kernel(const float* __restrict__ partial, int splits, int64_t n8,
+                                                         uint4* __restrict__ dwg, uint4* __restrict__ dwu) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= 2 * n8) return;
+  float v[8] = {};
+  for (int s = 0; s < splits; ++s) {
+    const float4* q = reinterpret_cast<const float4*>(partial) + ((size_t)s * 2 * n8 + i) * 2;
+    const float4 x = __ldcs(q), y = __ldcs(q + 1);
+    v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+    v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+  }
+  const uint4 o = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+  if (i < n8) dwg[i] = o;
+  else dwu[i - n8] = o;
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -357,7 +577,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ CUtensorMap
 // one.  No shared-memory stage, no barrier in the loop: with UN steps unrolled
 // a lane keeps 2 RT UN 16-byte loads in flight.  The warps' sums meet in
 // shared memory in a fixed order.
-constexpr int kFewTokens = 32;
+constexpr int kFewTokens = 8;
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
@@ -473,9 +693,7 @@ __global__ void __launch_bounds__(256) ffn_few_kernel(const FewParams p) {
 
 template <bool E4M3, int ACT>
 static moga_status launch_few(const FewParams& p, const char* who, cudaStream_t s) {
-  if (p.N <= 8) ffn_few_kernel<E4M3, ACT, 1, 1, 8><<<ceil_div(p.F, 8), 256, 0, s>>>(p);
-  else if (p.N <= 16) ffn_few_kernel<E4M3, ACT, 2, 2, 4><<<ceil_div(p.F, 16), 256, 0, s>>>(p);
-  else ffn_few_kernel<E4M3, ACT, 2, 4, 4><<<ceil_div(p.F, 16), 256, 0, s>>>(p);
+  ffn_few_kernel<E4M3, ACT, 1, 1, 8><<<ceil_div(p.F, 8), 256, 0, s>>>(p);
   return check_launch(who);
 }
 
@@ -495,19 +713,19 @@ static moga_status make_map(CUtensorMap* m, const void* base, int64_t rows, int6
   return MOGA_OK;
 }
 
-template <int MODE, bool E4M3, int ACT>
-static moga_status launch(const Params& p, const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b0,
-                          const CUtensorMap& b1, const char* who, cudaStream_t s) {
-  auto* k = ffn_kernel<MODE, E4M3, ACT>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+template <int MODE, bool E4M3, int ACT, int BN, int HM, int EW>
+static moga_status launch(const Params& p, const Maps& maps, int pairs, const char* who, cudaStream_t s) {
+  auto* k = ffn_kernel<MODE, E4M3, ACT, BN, HM, EW>;
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN, HM>::kSmemBytes);
   if (e != cudaSuccess) return fail(MOGA_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
-  // one pair of CTAs per pair of SMs (persistent), at most one pair per tile
-  const int pairs = std::min(p.total, route_tc::sm_count() / 2);
-  k<<<2 * pairs, kThreads, kSmemBytes, s>>>(p, a0, a1, b0, b1);
+  k<<<2 * pairs, (EW + 2) * 32, Tile<BN, HM>::kSmemBytes, s>>>(p, maps);
   return check_launch(who);
 }
 
 inline int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// one pair of CTAs per pair of SMs (persistent)
+inline int pair_count(int sms) { return sms / 2 > 0 ? sms / 2 : 1; }
 
 static moga_status check_dims(const char* who, int64_t N, int32_t d, int32_t F, int32_t act, int elem) {
   const int m = 16 / elem;   // 16-byte rows, as the TMA copies need them
@@ -515,18 +733,109 @@ static moga_status check_dims(const char* who, int64_t N, int32_t d, int32_t F, 
   if (d <= 0 || d % m != 0)
     return fail(MOGA_ERR_INVALID_ARG, "%s: d=%d must be a positive multiple of %d", who, d, m);
   if (F <= 0 || F % 8 != 0) return fail(MOGA_ERR_INVALID_ARG, "%s: F=%d must be a positive multiple of 8", who, F);
-  if (d > (1 << 20) || F > (1 << 20) || ceil64(N, 256) * ceil64(F, 128) > INT32_MAX / 2)
+  if (d > (1 << 20) || F > (1 << 20) || ceil64(N, 256) * ceil64(F, 32) > INT32_MAX / 2)
     return fail(MOGA_ERR_INVALID_ARG, "%s: sizes out of range", who);
   if (act != MOGA_ACT_SILU && act != MOGA_ACT_GELU)
     return fail(MOGA_ERR_INVALID_ARG, "%s: activation %d unknown", who, act);
   return MOGA_OK;
 }
 
+// The gated product over all tokens with tiles of BN accumulator columns.
+template <int MODE, bool E4M3, int BN>
+static moga_status launch_gated_bn(Params p, const void* x, const void* wg, const void* wu, int d, void* o0, void* o1,
+                                   int sms, const char* who, cudaStream_t s) {
+  constexpr int elem = E4M3 ? 1 : 2;
+  Maps maps;
+  moga_status st;
+  p.a_box = std::min(BM, ceil_div(p.rows, 32) * 32);
+  if ((st = make_map(&maps.m[0], x, p.rows, d, elem, p.a_box)) != MOGA_OK) return st;
+  if ((st = make_map(&maps.m[1], wg, p.cols, d, elem, BN / 2)) != MOGA_OK) return st;
+  if ((st = make_map(&maps.m[2], wu, p.cols, d, elem, BN / 2)) != MOGA_OK) return st;
+  maps.m[3] = maps.m[4] = maps.m[0];
+  if ((st = make_map(&maps.out[0], o0, p.rows, p.cols, 2, 32)) != MOGA_OK) return st;
+  maps.out[1] = maps.out[2] = maps.out[0];
+  if (MODE == MODE_DGDU && (st = make_map(&maps.out[1], o1, p.rows, p.cols, 2, 32)) != MOGA_OK) return st;
+  p.n_k = ceil_div(d, kRowBytes / elem);
+  p.m_tiles = ceil_div(p.rows, 2 * BM);
+  p.n_tiles = ceil_div(p.cols, BN / 2);
+  p.total = p.m_tiles * p.n_tiles;
+  const int pairs = std::min(p.total, pair_count(sms));
+  return p.act == MOGA_ACT_SILU ? launch<MODE, E4M3, MOGA_ACT_SILU, BN, 1, 4>(p, maps, pairs, who, s)
+                                : launch<MODE, E4M3, MOGA_ACT_GELU, BN, 1, 4>(p, maps, pairs, who, s);
+}
+
+// Accumulator columns of a gated tile for the given sizes: 128 where that
+// saves rounds.  A stage costs about 600 + BN of the same unit (BN = 256 and
+// 128 measured 391 and 333 ns a stage with few tokens: the 256 rows of A cost
+// what they cost), so the narrow tile pays only where it fills idle pairs.
+inline int pick_bn(int64_t N, int F, int sms) {
+  const int64_t mt = ceil64(N, 2 * BM);
+  const int P = pair_count(sms);
+  return ceil64(mt * ceil64(F, 64), P) * (600 + 128) < ceil64(mt * ceil64(F, 128), P) * (600 + 256) ? 128 : 256;
+}
+
+// The gated product; o1 is DGDU's second output (FWD: o0 again).
 template <int MODE, bool E4M3>
-static moga_status launch_act(const Params& p, const CUtensorMap& a0, const CUtensorMap& b0, const CUtensorMap& b1,
-                              const char* who, cudaStream_t s) {
-  return p.act == MOGA_ACT_SILU ? launch<MODE, E4M3, MOGA_ACT_SILU>(p, a0, a0, b0, b1, who, s)
-                                : launch<MODE, E4M3, MOGA_ACT_GELU>(p, a0, a0, b0, b1, who, s);
+static moga_status launch_gated(const Params& p, const void* x, const void* wg, const void* wu, int d, void* o0,
+                                void* o1, const char* who, cudaStream_t s) {
+  const int sms = route_tc::sm_count();
+  return pick_bn(p.rows, p.cols, sms) == 256 ? launch_gated_bn<MODE, E4M3, 256>(p, x, wg, wu, d, o0, o1, sms, who, s)
+                                             : launch_gated_bn<MODE, E4M3, 128>(p, x, wg, wu, d, o0, o1, sms, who, s);
+}
+
+constexpr int kGradBN = 256;
+
+// Rows of a gradient tile in 256s: 512-row tiles read a quarter less operand
+// bytes per product, 256-row tiles give twice the units.  Depends on the sizes
+// alone, as the splits below, so the workspace does too.
+inline int grad_hm(int64_t N, int d, int F, int sms) {
+  const int64_t nt = ceil64(d, kGradBN);
+  return nt * (ceil64(N, 4 * BM) + 2 * ceil64(F, 4 * BM)) >= 3 * (int64_t)pair_count(sms) / 2 ? 2 : 1;
+}
+// Splits of dW's K: none where its tiles keep at least half of the pairs busy
+// (dx tiles fill the rest), else enough for about one unit per pair, of at
+// least 4 stages each.
+inline int dw_split_stages(int64_t N, int d, int F, int sms) {
+  const int P = pair_count(sms);
+  const int64_t tiles = 2 * ceil64(F, 2 * grad_hm(N, d, F, sms) * BM) * ceil64(d, kGradBN);
+  const int kdw = (int)ceil64(N, 64);
+  if (2 * tiles >= P) return kdw;
+  const int s = std::max(1, std::min((int)(P / tiles), kdw / 4));
+  return ceil_div(kdw, s);
+}
+inline size_t dgdu_bytes(int64_t N, int F) { return ((size_t)2 * N * F * 2 + 255) / 256 * 256; }
+inline size_t grad_ws_bytes(int64_t N, int d, int F, int sms) {
+  const int splits = ceil_div((int)ceil64(N, 64), dw_split_stages(N, d, F, sms));
+  return dgdu_bytes(N, F) + (splits > 1 ? (size_t)splits * 2 * F * d * sizeof(float) : 0);
+}
+
+// The gradient units' shares (see unit_of).  Returns the number of pairs.
+inline int plan_grad(Params& p, int64_t N, int d, int F, bool need_dx, bool need_dw, int sms) {
+  p.rows = (int)N;
+  p.cols = d;
+  p.F = F;
+  const int rows = 2 * grad_hm(N, d, F, sms) * BM;
+  p.m_tiles = (int)ceil64(N, rows);
+  p.mf_tiles = ceil_div(F, rows);
+  p.n_tiles = ceil_div(d, kGradBN);
+  p.seg_k = ceil_div(F, 64);
+  p.kdw = (int)ceil64(N, 64);
+  p.kc = dw_split_stages(N, d, F, sms);
+  p.n_dw = need_dw ? 2 * p.mf_tiles * p.n_tiles * ceil_div(p.kdw, p.kc) : 0;
+  p.n_dx = need_dx ? p.m_tiles * p.n_tiles : 0;
+  const int P = (int)std::min<int64_t>((int64_t)p.n_dw + p.n_dx, pair_count(sms));
+  p.n1 = p.n_dw % P;
+  const int lag = ceil_div(p.kc, 2 * p.seg_k);   // dx tiles in the time of a dW unit
+  auto holds = [&](int b) { return (int64_t)p.n1 * std::max(0, b - lag) + (int64_t)(P - p.n1) * b >= p.n_dx; };
+  int lo = 0, hi = p.n_dx;
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (holds(mid)) hi = mid;
+    else lo = mid + 1;
+  }
+  p.b = lo;
+  p.a = p.n1 ? std::max(0, lo - lag) : lo;
+  return P;
 }
 
 }  // namespace ffn
@@ -569,30 +878,22 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
       return f8 ? launch_few<true, MOGA_ACT_SILU>(q, who, s) : launch_few<false, MOGA_ACT_SILU>(q, who, s);
     return f8 ? launch_few<true, MOGA_ACT_GELU>(q, who, s) : launch_few<false, MOGA_ACT_GELU>(q, who, s);
   }
-  CUtensorMap mx, mg, mu;
-  if ((st = make_map(&mx, x, N, d, elem, ffn::BM)) != MOGA_OK) return st;
-  if ((st = make_map(&mg, w_gate, F, d, elem, ffn::BN / 2)) != MOGA_OK) return st;
-  if ((st = make_map(&mu, w_up, F, d, elem, ffn::BN / 2)) != MOGA_OK) return st;
   ffn::Params p = {};
   p.rows = (int)N;
   p.cols = F;
-  p.n_k = ceil_div(d, kRowBytes / elem);
-  p.m_tiles = ceil_div((int)N, 2 * ffn::BM);
-  p.n_tiles = ceil_div(F, ffn::BN / 2);
-  p.total = p.m_tiles * p.n_tiles;
   p.act = act;
   p.xs = x_scale;
   p.gs = w_gate_scale;
   p.us = w_up_scale;
-  p.o0 = static_cast<__nv_bfloat16*>(out);
   p.timeout = kWaitLimitCycles;
-  return f8 ? launch_act<MODE_FWD, true>(p, mx, mg, mu, who, s) : launch_act<MODE_FWD, false>(p, mx, mg, mu, who, s);
+  return f8 ? launch_gated<MODE_FWD, true>(p, x, w_gate, w_up, d, out, out, who, s)
+            : launch_gated<MODE_FWD, false>(p, x, w_gate, w_up, d, out, out, who, s);
 }
 
 extern "C" size_t moga_gated_ffn_bwd_ws_bytes(int64_t N, int32_t d, int32_t F) {
   if (N <= 0 || N > INT32_MAX / 2 || d <= 0 || d % 8 != 0 || F <= 0 || F % 8 != 0 || d > (1 << 20) || F > (1 << 20))
     return 0;
-  return (size_t)2 * N * F * 2;
+  return moga::ffn::grad_ws_bytes(N, d, F, moga::route_tc::sm_count());
 }
 
 extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, const void* w_up, int64_t N, int32_t d,
@@ -609,12 +910,13 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
   if (st != MOGA_OK) return st;
   if (ceil64(N, 256) * ceil64(d, 256) > INT32_MAX / 2)
     return fail(MOGA_ERR_INVALID_ARG, "%s: sizes out of range", who);
-  const uintptr_t a = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_gate) |
-                      reinterpret_cast<uintptr_t>(w_up) | reinterpret_cast<uintptr_t>(dout) |
-                      reinterpret_cast<uintptr_t>(dx) | reinterpret_cast<uintptr_t>(dw_gate) |
-                      reinterpret_cast<uintptr_t>(dw_up) | reinterpret_cast<uintptr_t>(ws);
-  if (a & 15) return fail(MOGA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
-  const size_t need = moga_gated_ffn_bwd_ws_bytes(N, d, F);
+  const uintptr_t al = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_gate) |
+                       reinterpret_cast<uintptr_t>(w_up) | reinterpret_cast<uintptr_t>(dout) |
+                       reinterpret_cast<uintptr_t>(dx) | reinterpret_cast<uintptr_t>(dw_gate) |
+                       reinterpret_cast<uintptr_t>(dw_up) | reinterpret_cast<uintptr_t>(ws);
+  if (al & 15) return fail(MOGA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
+  const int sms = route_tc::sm_count();
+  const size_t need = grad_ws_bytes(N, d, F, sms);
   if (ws_bytes < need) return fail(MOGA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* dg = static_cast<__nv_bfloat16*>(ws);
@@ -622,52 +924,58 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
   ffn::Params p = {};
   p.act = act;
   p.timeout = kWaitLimitCycles;
-  {
-    CUtensorMap mx, mg, mu;
-    if ((st = make_map(&mx, x, N, d, 2, ffn::BM)) != MOGA_OK) return st;
-    if ((st = make_map(&mg, w_gate, F, d, 2, ffn::BN / 2)) != MOGA_OK) return st;
-    if ((st = make_map(&mu, w_up, F, d, 2, ffn::BN / 2)) != MOGA_OK) return st;
-    p.rows = (int)N;
-    p.cols = F;
-    p.n_k = ceil_div(d, 64);
-    p.m_tiles = ceil_div((int)N, 2 * ffn::BM);
-    p.n_tiles = ceil_div(F, ffn::BN / 2);
-    p.total = p.m_tiles * p.n_tiles;
-    p.dh = static_cast<const __nv_bfloat16*>(dout);
-    p.o0 = dg;
-    p.o1 = du;
-    if ((st = launch_act<MODE_DGDU, false>(p, mx, mg, mu, who, s)) != MOGA_OK) return st;
-  }
-  if (dx) {
-    CUtensorMap ma0, ma1, mb0, mb1;
-    if ((st = make_map(&ma0, dg, N, F, 2, ffn::BM)) != MOGA_OK) return st;
-    if ((st = make_map(&ma1, du, N, F, 2, ffn::BM)) != MOGA_OK) return st;
-    if ((st = make_map(&mb0, w_gate, F, d, 2, 64)) != MOGA_OK) return st;
-    if ((st = make_map(&mb1, w_up, F, d, 2, 64)) != MOGA_OK) return st;
-    p.rows = (int)N;
-    p.cols = d;
-    p.seg_k = ceil_div(F, 64);
-    p.n_k = 2 * p.seg_k;
-    p.m_tiles = ceil_div((int)N, 2 * ffn::BM);
-    p.n_tiles = ceil_div(d, ffn::BN);
-    p.total = p.m_tiles * p.n_tiles;
-    p.o0 = static_cast<__nv_bfloat16*>(dx);
-    if ((st = launch<MODE_DX, false, 0>(p, ma0, ma1, mb0, mb1, who, s)) != MOGA_OK) return st;
-  }
-  if (dw_gate) {
-    CUtensorMap ma0, ma1, mb;
-    if ((st = make_map(&ma0, dg, N, F, 2, 64)) != MOGA_OK) return st;
-    if ((st = make_map(&ma1, du, N, F, 2, 64)) != MOGA_OK) return st;
-    if ((st = make_map(&mb, x, N, d, 2, 64)) != MOGA_OK) return st;
-    p.rows = F;
-    p.cols = d;
-    p.n_k = ceil_div((int)N, 64);
-    p.m_tiles = ceil_div(F, 2 * ffn::BM);
-    p.n_tiles = ceil_div(d, ffn::BN);
-    p.total = 2 * p.m_tiles * p.n_tiles;
-    p.o0 = static_cast<__nv_bfloat16*>(dw_gate);
-    p.o1 = static_cast<__nv_bfloat16*>(dw_up);
-    if ((st = launch<MODE_DW, false, 0>(p, ma0, ma1, mb, mb, who, s)) != MOGA_OK) return st;
+  p.rows = (int)N;
+  p.cols = F;
+  p.dh = static_cast<const __nv_bfloat16*>(dout);
+  if ((st = launch_gated<MODE_DGDU, false>(p, x, w_gate, w_up, d, dg, du, who, s)) != MOGA_OK) return st;
+  const int pairs = plan_grad(p, N, d, F, dx != nullptr, dw_gate != nullptr, sms);
+  const int splits = ceil_div(p.kdw, p.kc);
+  p.partial = splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dgdu_bytes(N, F)) : nullptr;
+  ffn::Maps maps;
+  const void* base[5] = {x, w_gate, w_up, dg, du};
+  const int64_t rows[5] = {N, F, F, N, N}, cols[5] = {d, d, d, F, F};
+  for (int i = 0; i < 5; ++i)
+    if ((st = make_map(&maps.m[i], base[i], rows[i], cols[i], 2, 64)) != MOGA_OK) return st;
+  // a gradient that is not asked for has no unit: its map is never used
+  void* outs[3] = {dx ? dx : dw_gate, dw_gate ? dw_gate : dx, dw_up ? dw_up : dx};
+  const int64_t out_rows[3] = {dx ? N : F, dw_gate ? F : N, dw_up ? F : N};
+  for (int i = 0; i < 3; ++i)
+    if ((st = make_map(&maps.out[i], outs[i], out_rows[i], d, 2, 32)) != MOGA_OK) return st;
+  st = grad_hm(N, d, F, sms) == 2 ? launch<MODE_GRAD, false, 0, kGradBN, 2, 8>(p, maps, pairs, who, s)
+                                  : launch<MODE_GRAD, false, 0, kGradBN, 1, 8>(p, maps, pairs, who, s);
+  if (st != MOGA_OK) return st;
+  if (dw_gate && splits > 1) {
+    const int64_t n8 = (int64_t)F * d / 8;
+    ffn_dw_sum_kernel<<<(unsigned)ceil64(2 * n8, 256), 256, 0, s>>>(p.partial, splits, n8, static_cast<uint4*>(dw_gate),
+                                                                   static_cast<uint4*>(dw_up));
+    return check_launch(who);
   }
   return MOGA_OK;
+}
+
+// test hook (moga_testing.h): the units of every pair of one launch
+extern "C" int64_t moga_test_ffn_units(int32_t grad, int64_t N, int32_t d, int32_t F, int32_t need_dx,
+                                       int32_t need_dw, int32_t bn, int32_t sms, int32_t* out, int64_t cap) {
+  using namespace moga;
+  using namespace moga::ffn;
+  ffn::Params p = {};
+  int P;
+  if (grad) {
+    P = plan_grad(p, N, d, F, need_dx != 0, need_dw != 0, sms);
+  } else {
+    p.n_k = ceil_div(d, 64);
+    p.m_tiles = (int)ceil64(N, 2 * ffn::BM);
+    p.n_tiles = ceil_div(F, bn / 2);
+    p.total = p.m_tiles * p.n_tiles;
+    P = std::min(p.total, pair_count(sms));
+  }
+  int64_t n = 0;
+  ffn::Unit u;
+  for (int pair = 0; pair < P; ++pair)
+    for (int j = 0; grad ? unit_of<MODE_GRAD>(p, pair, P, j, &u) : unit_of<MODE_FWD>(p, pair, P, j, &u); ++j, ++n)
+      if (n < cap) {
+        const int32_t v[8] = {pair, u.kind, u.up, u.m, u.n, u.split, u.k0, u.k1};
+        for (int i = 0; i < 8; ++i) out[8 * n + i] = v[i];
+      }
+  return n;
 }
