@@ -485,7 +485,8 @@ moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const void* h, m
  * act:          MOGA_ACT_SILU or MOGA_ACT_GELU
  * out:          [N][F] bf16, written
  * Requires d % 8 == 0 (e4m3: d % 16 == 0), F % 8 == 0, d, F <= 2^20, N < 2^30
- * and 16-byte aligned x, w_gate, w_up, out.  Needs no workspace. */
+ * and 16-byte aligned x, w_gate, w_up, their scales and out.  Needs no
+ * workspace. */
 moga_status moga_gated_ffn(const void* x, const void* w_gate, const void* w_up, moga_dtype dt,
                            const float* x_scale, const float* w_gate_scale, const float* w_up_scale,
                            int64_t N, int32_t d, int32_t F, int32_t act, void* out, void* stream);

@@ -21,9 +21,9 @@
 //   dx and dW share one launch (see "gradient units"), of 512-row tiles where
 //   there are enough of them.
 //
-// 320 threads per CTA: warps 0-7 epilogue (thread = TMEM lane of its warp's
-// quarter, two warps per quarter with half of the columns each), warp 8 TMA
-// producer, warp 9 TMEM allocator and (leader) MMA issuer.  Two accumulators
+// EW + 2 warps per CTA: warps 0 to EW - 1 (4 or 8) epilogue (thread = TMEM lane
+// of its warp's quarter; with 8 warps two share a quarter and halve its
+// columns), one TMA producer, one TMEM allocator and (leader) MMA issuer.  Two accumulators
 // of BN columns let a tile's epilogue overlap the next tile's products.  All
 // waits are bounded.
 #include "common.cuh"
@@ -223,31 +223,46 @@ __device__ __forceinline__ void boxes_free(int lane) {
   __syncwarp();
 }
 
-// A gated tile's BN / 2 columns for the warp's 32 rows from row0.  `turn`
-// counts the warp's stores: its two boxes are filled in turn.
-template <bool E4M3, int ACT, int BN>
+// A warp gives its accumulator back on the leader's barrier, once per tile:
+// as soon as the last values are in registers, so that the next tile's products
+// do not wait for this one's arithmetic and stores.
+__device__ __forceinline__ void release_acc(uint32_t empty, int lane) {
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(empty) : "memory");
+}
+
+// COLS columns of a gated tile from c_begin, for the warp's 32 rows from row0.
+// `turn` counts the warp's stores: its BOXES boxes are filled in turn.
+template <bool E4M3, int ACT, int BN, int COLS, int BOXES>
 __device__ __forceinline__ void epilogue_fwd(const Params& p, const CUtensorMap* map, uint32_t acc, uint32_t boxes,
-                                             int row0, int col0, int lane, int& turn) {
+                                             int row0, int col0, int c_begin, int lane, int& turn, uint32_t empty) {
   const int row = row0 + lane;
   const float xs = E4M3 && row < p.rows ? __ldg(p.xs + row) : 1.f;
 #pragma unroll 1
-  for (int c0 = 0; c0 < BN / 2; c0 += 64) {
+  for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 64) {
     const int col = col0 + c0;
-    if (col >= p.cols || row0 >= p.rows) break;   // the whole warp
-    const uint32_t box = boxes + (turn++ & 1) * kOutBox;
-    boxes_free<1>(lane);
+    if (col >= p.cols || row0 >= p.rows) {   // the whole warp
+      release_acc(empty, lane);
+      break;
+    }
+    const uint32_t box = boxes + (turn++ % BOXES) * kOutBox;
+    boxes_free<BOXES - 1>(lane);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       float g[32], u[32];
       tmem_ld32(acc + c0 + 32 * h, g);
       tmem_ld32(acc + BN / 2 + c0 + 32 * h, u);
       tmem_wait_ld();
+      if (h == 1 && c0 + 64 >= c_begin + COLS) release_acc(empty, lane);
       if (E4M3) {
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const int cc = min(col + 32 * h + j, p.cols - 1);
-          g[j] *= xs * __ldg(p.gs + cc);
-          u[j] *= xs * __ldg(p.us + cc);
+        for (int e = 0; e < 8; ++e) {
+          const int cc = min(col + 32 * h + 4 * e, p.cols - 4);   // F is a multiple of 8
+          const float4 a = __ldg(reinterpret_cast<const float4*>(p.gs + cc));
+          const float4 b = __ldg(reinterpret_cast<const float4*>(p.us + cc));
+          g[4 * e] *= xs * a.x; g[4 * e + 1] *= xs * a.y; g[4 * e + 2] *= xs * a.z; g[4 * e + 3] *= xs * a.w;
+          u[4 * e] *= xs * b.x; u[4 * e + 1] *= xs * b.y; u[4 * e + 2] *= xs * b.z; u[4 * e + 3] *= xs * b.w;
         }
       }
 #pragma unroll
@@ -273,11 +288,15 @@ __device__ __forceinline__ void load_dout(const Params& p, int row0, int col, in
 // dout (loaded before the products were waited for).
 template <int ACT, int BN>
 __device__ __forceinline__ void epilogue_dgdu(const Params& p, const CUtensorMap* mg, const CUtensorMap* mu,
-                                              uint32_t acc, uint32_t boxes, int row0, int col0, int lane, uint4* v) {
+                                              uint32_t acc, uint32_t boxes, int row0, int col0, int lane, uint4* v,
+                                              uint32_t empty) {
 #pragma unroll 1
   for (int c0 = 0; c0 < BN / 2; c0 += 64) {
     const int col = col0 + c0;
-    if (col >= p.cols || row0 >= p.rows) break;   // the whole warp
+    if (col >= p.cols || row0 >= p.rows) {   // the whole warp
+      release_acc(empty, lane);
+      break;
+    }
     if (c0 > 0) load_dout(p, row0, col, lane, v);
     boxes_free<0>(lane);
     // dout from lanes of columns to lanes of rows, through the first box
@@ -296,6 +315,7 @@ __device__ __forceinline__ void epilogue_dgdu(const Params& p, const CUtensorMap
       tmem_ld32(acc + c0 + 32 * h, g);
       tmem_ld32(acc + BN / 2 + c0 + 32 * h, u);
       tmem_wait_ld();
+      if (h == 1 && c0 + 64 >= BN / 2) release_acc(empty, lane);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float d = __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
@@ -316,12 +336,15 @@ __device__ __forceinline__ void epilogue_dgdu(const Params& p, const CUtensorMap
 // bf16 through the box, or the fp32 partial sum where K is split.
 template <int BN, int COLS>
 __device__ __forceinline__ void epilogue_grad(const Params& p, const CUtensorMap* map, const Unit& u, uint32_t acc,
-                                              uint32_t box, int row0, int c_begin, int lane) {
+                                              uint32_t box, int row0, int c_begin, int lane, uint32_t empty) {
   const int rows = u.kind == 1 ? p.rows : p.F;
 #pragma unroll 1
   for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 64) {
     const int col = u.n * BN + c0;
-    if (col >= p.cols || row0 >= rows) break;   // the whole warp
+    if (col >= p.cols || row0 >= rows) {   // the whole warp
+      release_acc(empty, lane);
+      break;
+    }
     const bool split = u.kind == 2 && p.partial;
     if (!split) boxes_free<0>(lane);
 #pragma unroll
@@ -329,6 +352,7 @@ __device__ __forceinline__ void epilogue_grad(const Params& p, const CUtensorMap
       float v[32];
       tmem_ld32(acc + c0 + 32 * h, v);
       tmem_wait_ld();
+      if (h == 1 && c0 + 64 >= c_begin + COLS) release_acc(empty, lane);
       if (!split) {
         put32(box, lane, h, v);
       } else if (row0 + lane < rows) {
@@ -520,16 +544,16 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
 #pragma unroll 1
       for (int h = 0; h < HM; ++h) {
         const uint32_t acc = tmem + lane_addr + (HM == 1 ? b : h) * BN;
+        const uint32_t empty = peer_addr(bar(T::kAccEmpty + (HM == 1 ? b : h)), 0);
         if constexpr (MODE == MODE_FWD)
-          epilogue_fwd<E4M3, ACT, BN>(p, &maps.out[0], acc, boxes, row0, u.n * (BN / 2), lane, turn);
+          epilogue_fwd<E4M3, ACT, BN, BN * 2 / EW, 8 / EW>(p, &maps.out[0], acc, boxes, row0, u.n * (BN / 2),
+                                                           half * (BN * 2 / EW), lane, turn, empty);
         else if constexpr (MODE == MODE_DGDU)
-          epilogue_dgdu<ACT, BN>(p, &maps.out[0], &maps.out[1], acc, boxes, row0, u.n * (BN / 2), lane, v);
+          epilogue_dgdu<ACT, BN>(p, &maps.out[0], &maps.out[1], acc, boxes, row0, u.n * (BN / 2), lane, v,
+                                 empty);
         else
           epilogue_grad<BN, BN * 4 / EW>(p, &maps.out[u.kind == 1 ? 0 : 1 + u.up], u, acc, boxes, row0 + h * BM,
-                                         half * (BN * 4 / EW), lane);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(peer_addr(bar(T::kAccEmpty + (HM == 1 ? b : h)), 0));
+                                         half * (BN * 4 / EW), lane, empty);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -760,8 +784,11 @@ static moga_status launch_gated_bn(Params p, const void* x, const void* wg, cons
   p.n_tiles = ceil_div(p.cols, BN / 2);
   p.total = p.m_tiles * p.n_tiles;
   const int pairs = std::min(p.total, pair_count(sms));
-  return p.act == MOGA_ACT_SILU ? launch<MODE, E4M3, MOGA_ACT_SILU, BN, 1, 4>(p, maps, pairs, who, s)
-                                : launch<MODE, E4M3, MOGA_ACT_GELU, BN, 1, 4>(p, maps, pairs, who, s);
+  // Warps of the epilogue: eight, with half of the columns each, where a half
+  // is a box wide and a warp needs only one.
+  constexpr int EW = MODE == MODE_FWD && BN == 256 ? 8 : 4;
+  return p.act == MOGA_ACT_SILU ? launch<MODE, E4M3, MOGA_ACT_SILU, BN, 1, EW>(p, maps, pairs, who, s)
+                                : launch<MODE, E4M3, MOGA_ACT_GELU, BN, 1, EW>(p, maps, pairs, who, s);
 }
 
 // Accumulator columns of a gated tile for the given sizes: 128 where that
@@ -857,10 +884,9 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
   if (st != MOGA_OK) return st;
   const uintptr_t a = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_gate) |
                       reinterpret_cast<uintptr_t>(w_up) | reinterpret_cast<uintptr_t>(out);
-  const uintptr_t a4 = reinterpret_cast<uintptr_t>(x_scale) | reinterpret_cast<uintptr_t>(w_gate_scale) |
-                       reinterpret_cast<uintptr_t>(w_up_scale);
-  if ((a & 15) || (a4 & 3))
-    return fail(MOGA_ERR_INVALID_ARG, "%s: x, w_gate, w_up, out must be 16-byte aligned", who);
+  const uintptr_t ws = reinterpret_cast<uintptr_t>(w_gate_scale) | reinterpret_cast<uintptr_t>(w_up_scale);
+  if (((a | ws) & 15) || (reinterpret_cast<uintptr_t>(x_scale) & 3))
+    return fail(MOGA_ERR_INVALID_ARG, "%s: x, w_gate, w_up, their scales and out must be 16-byte aligned", who);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (N <= kFewTokens) {
     FewParams q = {};
