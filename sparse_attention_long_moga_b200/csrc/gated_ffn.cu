@@ -591,16 +591,20 @@ __global__ void __launch_bounds__(256) ffn_dw_sum_kernel(const float* __restrict
 // ---------------------------------------------------------------- few tokens
 //
 // Up to kFewTokens tokens the weights' read is the time (2 F d elements for
-// N d + N F others), and a 256-row tile would idle.  A CTA takes 8 RT columns
-// of F and all tokens; its 8 warps split d, each streaming 64-byte pieces of
-// 16 RT weight rows straight from global memory into mma.sync fragments: one
-// 16-row A tile is 8 gate rows over the 8 up rows of the same columns, so a
-// lane's accumulators hold gate and up of the same outputs.  A lane loads 16
+// N d + N F others), and a 256-row tile would idle.  A CTA takes 8 columns of
+// F and all tokens; its W warps split d, each streaming 64-byte pieces of 16
+// weight rows straight from global memory into mma.sync fragments: the 16-row
+// A tile is 8 gate rows over the 8 up rows of the same columns, so a lane's
+// accumulators hold gate and up of the same outputs.  A lane loads 16
 // consecutive bytes of a row where the fragment wants four pieces spread over
 // k; the sum over k does not mind the order as long as x is read in the same
-// one.  No shared-memory stage, no barrier in the loop: with UN steps unrolled
-// a lane keeps 2 RT UN 16-byte loads in flight.  The warps' sums meet in
-// shared memory in a fixed order.
+// one.  No shared-memory stage, no barrier in the loop: a lane keeps 2 UN
+// 16-byte loads under way, and many small CTAs per SM do the rest (UN = 4,
+// W = 8 in bf16, UN = 8, W = 4 in e4m3: the fewest registers that hold the
+// loads of one pass over d = 1536 to 5120; twice the unrolling measured 47
+// instead of 43.5 us, half the warps 46).  One token through 5120 x 13824:
+// 43.5 us, the weights at the copy rate (6.5 TB/s); e4m3 27 us, 5.2 TB/s.
+// The warps' sums meet in shared memory in a fixed order.
 constexpr int kFewTokens = 8;
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
@@ -633,91 +637,63 @@ struct FewParams {
   __nv_bfloat16* out;
 };
 
-template <bool E4M3, int ACT, int RT, int NT, int UN>
-__global__ void __launch_bounds__(256) ffn_few_kernel(const FewParams p) {
-  constexpr int kCols = 8 * RT, kToks = 8 * NT;
-  __shared__ float red[8][RT * NT * 4][32];
+template <bool E4M3, int ACT, int UN, int W>
+__global__ void __launch_bounds__(32 * W) ffn_few_kernel(const FewParams p) {
+  __shared__ float red[W][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
-  const int f0 = blockIdx.x * kCols;
-  const uint8_t *wg[RT], *wu[RT], *xp[NT];
-  bool won[RT], xon[NT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r) {
-    const int f = f0 + 8 * r + g;
-    won[r] = f < p.F;
-    wg[r] = p.wg + (size_t)(won[r] ? f : 0) * p.row_bytes + 16 * q;
-    wu[r] = p.wu + (size_t)(won[r] ? f : 0) * p.row_bytes + 16 * q;
-  }
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    xon[n] = 8 * n + g < p.N;
-    xp[n] = p.x + (size_t)(xon[n] ? 8 * n + g : 0) * p.row_bytes + 16 * q;
-  }
-  float acc[RT][NT][4];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[r][n][i] = 0.f;
+  const int f0 = blockIdx.x * 8;                      // F is a multiple of 8: all rows exist
+  const uint8_t* wg = p.wg + (size_t)(f0 + g) * p.row_bytes + 16 * q;
+  const uint8_t* wu = p.wu + (size_t)(f0 + g) * p.row_bytes + 16 * q;
+  const bool xon = g < p.N;
+  const uint8_t* xp = p.x + (size_t)(xon ? g : 0) * p.row_bytes + 16 * q;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f};
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  // step s covers bytes [64 s, 64 s + 64) of every row; warp w takes s = w, w + 8, ...
-  for (int s0 = warp; 64 * s0 < p.row_bytes; s0 += 8 * UN) {
-    uint4 a[UN][RT], b[UN][RT], x[UN][NT];
+  // step s covers bytes [64 s, 64 s + 64) of every row; warp w takes s = w, w + W, ...
+  for (int s0 = warp; 64 * s0 < p.row_bytes; s0 += W * UN) {
+    uint4 a[UN], b[UN], x[UN];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
-      const int k = 64 * (s0 + 8 * i);
+      const int k = 64 * (s0 + W * i);
       const bool on = k + 16 * q < p.row_bytes;
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        a[i][r] = on && won[r] ? ldg_stream(wg[r] + k) : zero;
-        b[i][r] = on && won[r] ? ldg_stream(wu[r] + k) : zero;
-      }
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        x[i][n] = on && xon[n] ? __ldg(reinterpret_cast<const uint4*>(xp[n] + k)) : zero;
+      a[i] = on ? ldg_stream(wg + k) : zero;
+      b[i] = on ? ldg_stream(wu + k) : zero;
     }
 #pragma unroll
-    for (int i = 0; i < UN; ++i)
+    for (int i = 0; i < UN; ++i) {
+      const int k = 64 * (s0 + W * i);
+      x[i] = xon && k + 16 * q < p.row_bytes ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : zero;
+    }
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma_16x8<E4M3>(acc[r][n], a[i][r].x, b[i][r].x, a[i][r].y, b[i][r].y, x[i][n].x, x[i][n].y);
-          mma_16x8<E4M3>(acc[r][n], a[i][r].z, b[i][r].z, a[i][r].w, b[i][r].w, x[i][n].z, x[i][n].w);
-        }
+    for (int i = 0; i < UN; ++i) {
+      mma_16x8<E4M3>(acc, a[i].x, b[i].x, a[i].y, b[i].y, x[i].x, x[i].y);
+      mma_16x8<E4M3>(acc, a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
+    }
   }
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) red[warp][(r * NT + n) * 4 + i][lane] = acc[r][n][i];
+  for (int i = 0; i < 4; ++i) red[warp][i][lane] = acc[i];
   __syncthreads();
-  // output (column c, token t): accumulator of tile (c / 8, t / 8), lane 4 (c % 8) + (t % 8) / 2, slot t % 2 (gate),
-  // 2 + t % 2 (up)
-  for (int o = threadIdx.x; o < kCols * kToks; o += 256) {
-    const int c = o % kCols, t = o / kCols, f = f0 + c;
-    if (f >= p.F || t >= p.N) continue;
-    const int slot = ((c >> 3) * NT + (t >> 3)) * 4 + (t & 1), l = 4 * (c & 7) + ((t & 7) >> 1);
-    float gate = 0.f, up = 0.f;
+  // column c, token t: lane 4 c + t / 2, slot t % 2 (gate), 2 + t % 2 (up)
+  const int c = threadIdx.x & 7, t = threadIdx.x >> 3;
+  if (t >= p.N) return;
+  const int l = 4 * c + (t >> 1), slot = t & 1;
+  float gate = 0.f, up = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      gate += red[w][slot][l];
-      up += red[w][slot + 2][l];
-    }
-    if (E4M3) {
-      const float xs = __ldg(p.xs + t);
-      gate *= xs * __ldg(p.gs + f);
-      up *= xs * __ldg(p.us + f);
-    }
-    p.out[(size_t)t * p.F + f] = __float2bfloat16_rn(act_of<ACT>(gate) * up);
+  for (int w = 0; w < W; ++w) {
+    gate += red[w][slot][l];
+    up += red[w][slot + 2][l];
   }
+  if (E4M3) {
+    const float xs = __ldg(p.xs + t);
+    gate *= xs * __ldg(p.gs + f0 + c);
+    up *= xs * __ldg(p.us + f0 + c);
+  }
+  p.out[(size_t)t * p.F + f0 + c] = __float2bfloat16_rn(act_of<ACT>(gate) * up);
 }
 
 template <bool E4M3, int ACT>
 static moga_status launch_few(const FewParams& p, const char* who, cudaStream_t s) {
-  ffn_few_kernel<E4M3, ACT, 1, 1, 8><<<ceil_div(p.F, 8), 256, 0, s>>>(p);
+  constexpr int UN = E4M3 ? 8 : 4, W = E4M3 ? 4 : 8;
+  ffn_few_kernel<E4M3, ACT, UN, W><<<p.F / 8, 32 * W, 0, s>>>(p);
   return check_launch(who);
 }
 

@@ -6,8 +6,10 @@
 // y is taken from the stored h, so that the backward, which reads only h,
 // differentiates exactly what the forward computed.  The 8-bit output is
 //   scale = max(max|y|, 2^-100) / 448,  q = e4m3(y / scale)  per row;
-// y / scale = (h w) * 448 / max|h w| (r cancels), which needs one rounding
-// fewer and keeps q off the wrong side of a rounding border.
+// y / scale = (h w) * 448 / max|h w| (r cancels).  A value that fp32 puts on
+// the wrong side of a rounding border is off by a whole step of the 3-bit
+// mantissa; the few values that fall near one are computed again in two fp32
+// words, so that q is the e4m3 value nearest to the exact ratio.
 //
 // Backward, with dn = dy * w and c = r^2 * mean(dn * h):
 //   dx = r * (dn - h * c) + dres,   dw = sum over rows of dy * h * r
@@ -16,6 +18,8 @@
 // Bound: HBM.  Each row is read once into registers (8-element vectors, one
 // to five per thread) and written once; sums, the row statistics and dw are
 // fp32.  TPR threads share a row, 256 / TPR rows share a CTA.
+#include <algorithm>
+
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -95,31 +99,63 @@ __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
-}
-
 // Barrier of the TPR threads of one row (named barrier 1 + group).
 template <int TPR>
 __device__ __forceinline__ void row_sync(int group) {
   asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(TPR) : "memory");
 }
 
-// Sum (or maximum) over the TPR threads of a row, in the same order on every
-// thread.  `slots`: TPR / 32 floats of the row's own that no thread still
-// reads; consecutive calls take different slots.
-template <int TPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float* slots, int group, int lane_in_row) {
-  v = MAX ? warp_max(v) : warp_sum(v);
+// Sum over the TPR threads of a row, in the same order on every thread.
+// `slots`: TPR / 32 floats of the row's own.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float* slots, int group, int lane_in_row) {
+  v = warp_sum(v);
   if (TPR == 32) return v;
   if ((lane_in_row & 31) == 0) slots[lane_in_row >> 5] = v;
   row_sync<TPR>(group);
   float r = slots[0];
 #pragma unroll
-  for (int i = 1; i < TPR / 32; ++i) r = MAX ? fmaxf(r, slots[i]) : r + slots[i];
+  for (int i = 1; i < TPR / 32; ++i) r += slots[i];
   return r;
+}
+
+// The largest mx over the TPR threads of a row, with the me that goes with it
+// (the larger one where several share mx).
+template <int TPR>
+__device__ __forceinline__ void row_max_pair(float& mx, float& me, float* slots, float* slots_e, int group,
+                                             int lane_in_row) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), e2 = __shfl_xor_sync(0xffffffffu, me, o);
+    if (m2 > mx || (m2 == mx && e2 > me)) {
+      mx = m2;
+      me = e2;
+    }
+  }
+  if (TPR == 32) return;
+  if ((lane_in_row & 31) == 0) {
+    slots[lane_in_row >> 5] = mx;
+    slots_e[lane_in_row >> 5] = me;
+  }
+  row_sync<TPR>(group);
+  mx = slots[0];
+  me = slots_e[0];
+#pragma unroll
+  for (int i = 1; i < TPR / 32; ++i)
+    if (slots[i] > mx || (slots[i] == mx && slots_e[i] > me)) {
+      mx = slots[i];
+      me = slots_e[i];
+    }
+}
+
+// hi + lo (|lo| below an ulp or so of hi) as one fp32 value that a later
+// rounding to fewer bits rounds as it would the sum: the nearest value, moved
+// to its odd neighbour on the remainder's side where the sum is not exact.
+__device__ __forceinline__ float round_to_odd(float hi, float lo) {
+  const float s = hi + lo, rest = lo - (s - hi);
+  int b = __float_as_int(s);
+  if (rest != 0.f && !(b & 1)) b += (rest > 0.f) == (s > 0.f) ? 1 : -1;
+  return __int_as_float(b);
 }
 
 struct FwdParams {
@@ -139,7 +175,7 @@ __global__ void __launch_bounds__(kCtaThreads<TPR>)
 rms_norm_kernel(const FwdParams p) {
   constexpr int kGroups = kCtaThreads<TPR> / TPR;
   constexpr bool kQuant = sizeof(YT) == 1;
-  __shared__ float red[2][kGroups][TPR / 32];
+  __shared__ float red[3][kGroups][TPR / 32];
   const int group = threadIdx.x / TPR, li = threadIdx.x % TPR;
   const int row = blockIdx.x * kGroups + group;
   if (row >= p.N) return;   // whole rows leave together: the row barriers stay complete
@@ -173,9 +209,24 @@ rms_norm_kernel(const FwdParams p) {
       for (int j = 0; j < 8; ++j) ss += f[i][j] * f[i][j];
     }
   }
-  ss = row_reduce<TPR, false>(ss, red[0][group], group, li);
+  ss = row_sum<TPR>(ss, red[0][group], group, li);
   const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
-  float mx = 0.f;
+  if (!kQuant) {
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (v < nv) {
+        float w[8];
+        load_w(p.w, p.w_bf16, 8 * v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * rstd * w[j];
+        Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, f[i]);
+      }
+    }
+    return;
+  }
+  // f becomes t = h w rounded; the largest |t| and its remainder: max|h w| = mx + me
+  float mx = 0.f, me = 0.f;
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = li + i * TPR;
@@ -184,30 +235,49 @@ rms_norm_kernel(const FwdParams p) {
       load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        f[i][j] = kQuant ? f[i][j] * w[j] : f[i][j] * rstd * w[j];
-        if (kQuant) mx = fmaxf(mx, fabsf(f[i][j]));
-      }
-      if (!kQuant) Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, f[i]);
-    }
-  }
-  if (kQuant) {
-    mx = row_reduce<TPR, true>(mx, red[1][group], group, li);
-    const float amax = mx * rstd;                             // max|y|; NaN if the row holds NaN or infinity
-    const float top = amax < kScaleFloor ? kScaleFloor : amax;
-    // the short way where neither 448 / max|h w| nor the floor matters
-    const bool direct = amax >= kScaleFloor && mx >= kScaleFloor;
-    const float k1 = direct ? 1.f : rstd, k2 = kE4m3Max / (direct ? mx : top);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = li + i * TPR;
-      if (v < nv) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = (f[i][j] * k1) * k2;
-        Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, f[i]);
+        const float t = f[i][j] * w[j], e = fmaf(f[i][j], w[j], -t);
+        if (fabsf(t) > mx) {
+          mx = fabsf(t);
+          me = t < 0.f ? -e : e;
+        }
+        f[i][j] = t;
       }
     }
-    if (li == 0) p.scale[row] = top / kE4m3Max;
   }
+  row_max_pair<TPR>(mx, me, red[1][group], red[2][group], group, li);
+  const float amax = mx * rstd;                             // max|y|; NaN if the row holds NaN or infinity
+  const float top = amax < kScaleFloor ? kScaleFloor : amax;
+  // the short way where neither 448 / max|h w| nor the floor matters
+  const bool direct = amax >= kScaleFloor && mx >= kScaleFloor;
+  const float k1 = direct ? 1.f : rstd, k2 = kE4m3Max / (direct ? mx : top);
+#pragma unroll
+  for (int i = 0; i < VPT; ++i) {
+    const int v = li + i * TPR;
+    if (v < nv) {
+      bool near = false;
+      float q[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        q[j] = (f[i][j] * k1) * k2;
+        // within 8 units of a tie of the 3-bit mantissa; the four roundings above are worth 4 at most
+        near |= ((__float_as_uint(q[j]) + 8u) & 0xfffffu) - 0x80000u <= 16u;
+      }
+      if (near && direct) {   // 1 vector in 8000
+        const float k2lo = (fmaf(-k2, mx, kE4m3Max) - k2 * me) / mx;
+        float h[8], w[8];
+        if (RES) Vec<HT>::widen(Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v), h);
+        else Vec<XT>::widen(Vec<XT>::load(static_cast<const XT*>(p.x) + base + 8 * v), h);
+        load_w(p.w, p.w_bf16, 8 * v, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = f[i][j], hi = t * k2;
+          q[j] = round_to_odd(hi, fmaf(t, k2, -hi) + fmaf(t, k2lo, fmaf(h[j], w[j], -t) * k2));
+        }
+      }
+      Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, q);
+    }
+  }
+  if (li == 0) p.scale[row] = top / kE4m3Max;
 }
 
 struct BwdParams {
@@ -224,13 +294,19 @@ struct BwdParams {
 // dw in registers (each thread always sees the same columns), then adds its
 // row groups in shared memory and writes one partial row.  No atomics: every
 // sum runs in a fixed order, so dw is the same from run to run.
-template <int TPR, int VPT, class DT, class HT>
-__global__ void __launch_bounds__(kCtaThreads<TPR>)
+// GROUPS rows at a time, VPT vectors a thread.  Rows of up to 768 elements: a
+// warp a row, 8 rows a CTA.  Wider rows: a row a CTA of just enough threads, so
+// that an SM holds many rows in different phases and the loads of some are
+// under way while others are at their sums (bwd_shape).  63,960 x 1536, bf16
+// dy, fp32 h: 233 us, 6.7 TB/s, against 276 us of four rows a CTA with three
+// vectors a thread; bf16 h: 139 us, 5.7 TB/s.
+template <int GROUPS, int VPT, class DT, class HT>
+__global__ void __launch_bounds__(GROUPS > 1 ? 32 * GROUPS : VPT == 1 || (VPT == 2 && sizeof(HT) == 2) ? 1024 : 512)
 rms_norm_bwd_kernel(const BwdParams p) {
-  constexpr int kGroups = kCtaThreads<TPR> / TPR;
   extern __shared__ float s_dw[];                 // [d] when there is more than one group
-  __shared__ float red[2][2][kGroups][TPR / 32];
-  const int group = threadIdx.x / TPR, li = threadIdx.x % TPR;
+  __shared__ float2 red[2][32];
+  const int tpr = GROUPS > 1 ? 32 : blockDim.x;
+  const int group = GROUPS > 1 ? threadIdx.x / 32 : 0, li = GROUPS > 1 ? threadIdx.x % 32 : threadIdx.x;
   const int nv = p.d >> 3;
   float acc[VPT][8];
 #pragma unroll
@@ -238,13 +314,13 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
   int par = 0;
-  for (int row = blockIdx.x * kGroups + group; row < p.N; row += gridDim.x * kGroups, par ^= 1) {
+  for (int row = blockIdx.x * GROUPS + group; row < p.N; row += gridDim.x * GROUPS, par ^= 1) {
     const size_t base = (size_t)row * p.d;
     typename Vec<DT>::type dv[VPT];
     typename Vec<HT>::type hv[VPT], sv[VPT];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = li + i * TPR;
+      const int v = li + i * tpr;
       if (v < nv) {
         dv[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
         hv[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
@@ -254,7 +330,7 @@ rms_norm_bwd_kernel(const BwdParams p) {
     float ss = 0.f, dot = 0.f;
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = li + i * TPR;
+      const int v = li + i * tpr;
       if (v < nv) {
         float dy[8], h[8], w[8];
         Vec<DT>::widen(dv[i], dy);
@@ -263,35 +339,26 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           ss += h[j] * h[j];
-          dot += dy[j] * w[j] * h[j];
+          dot += dy[j] * h[j] * w[j];
         }
       }
     }
-    // both sums cross one barrier
     ss = warp_sum(ss);
     dot = warp_sum(dot);
-    if (TPR > 32) {
-      float* s0 = red[par][0][group];
-      float* s1 = red[par][1][group];
-      if ((li & 31) == 0) {
-        s0[li >> 5] = ss;
-        s1[li >> 5] = dot;
-      }
-      row_sync<TPR>(group);
-      ss = s0[0];
-      dot = s1[0];
-#pragma unroll
-      for (int i = 1; i < TPR / 32; ++i) {
-        ss += s0[i];
-        dot += s1[i];
-      }
+    if (GROUPS == 1) {   // both sums of the CTA's warps cross one barrier; the slots alternate, so one is enough
+      if ((threadIdx.x & 31) == 0) red[par][threadIdx.x >> 5] = make_float2(ss, dot);
+      __syncthreads();
+      const bool on = (threadIdx.x & 31) < (blockDim.x >> 5);
+      const float2 t = on ? red[par][threadIdx.x & 31] : make_float2(0.f, 0.f);
+      ss = warp_sum(t.x);
+      dot = warp_sum(t.y);
     }
     const float inv_d = 1.f / (float)p.d;
     const float rstd = 1.f / sqrtf(ss * inv_d + p.eps);
-    const float c = rstd * rstd * (dot * inv_d);
+    const float c = rstd * rstd * rstd * (dot * inv_d);
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      const int v = li + i * TPR;
+      const int v = li + i * tpr;
       if (v < nv) {
         float dy[8], h[8], w[8], o[8];
         Vec<DT>::widen(dv[i], dy);
@@ -299,8 +366,8 @@ rms_norm_bwd_kernel(const BwdParams p) {
         load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          o[j] = rstd * (dy[j] * w[j] - h[j] * c);
-          acc[i][j] += dy[j] * (h[j] * rstd);
+          o[j] = rstd * (dy[j] * w[j]) - c * h[j];
+          acc[i][j] += dy[j] * h[j] * rstd;
         }
         if (p.dres) {
           float s[8];
@@ -315,11 +382,11 @@ rms_norm_bwd_kernel(const BwdParams p) {
   }
   if (!p.partial) return;
   float* dst = p.partial + (size_t)blockIdx.x * p.d;
-  for (int g = 0; g < kGroups; ++g) {
+  for (int g = 0; g < GROUPS; ++g) {
     if (group == g) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        const int v = li + i * TPR;
+        const int v = li + i * tpr;
         if (v < nv) {
           if (g > 0) {
             float s[8];
@@ -327,11 +394,11 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] += s[j];
           }
-          Vec<float>::store(g == kGroups - 1 ? dst + 8 * v : s_dw + 8 * v, acc[i]);
+          Vec<float>::store(g == GROUPS - 1 ? dst + 8 * v : s_dw + 8 * v, acc[i]);
         }
       }
     }
-    if (kGroups > 1) __syncthreads();
+    if (GROUPS > 1) __syncthreads();
   }
 }
 
@@ -404,34 +471,42 @@ static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_
   return fail(MOGA_ERR_UNSUPPORTED, "moga_rms_norm: an fp32 output needs an fp32 stream");
 }
 
-inline int bwd_groups(int cfg) {
-  static const int g[6] = {8, 4, 4, 2, 1, 1};
-  return g[cfg];
+// Backward launch shape: threads of a CTA, vectors a thread, CTAs an SM holds.
+// All CTAs have to be resident at once (a second round of them costs a third),
+// so the last follows from the kernels' registers: 64 (one vector; two with a
+// bf16 h), up to 100 (two, fp32 h), 128 (three, four), 80 (warp a row, one).
+// Bytes on the way decide between one and two vectors: two where a bf16 row's
+// vectors are small or where one would leave an SM's threads unused
+// (32,760 x 5120, fp32 h: 526 us with one vector, 367 with two).
+struct BwdShape {
+  int threads, vpt, per_sm;
+};
+constexpr int kWarpRow = 768;
+inline BwdShape bwd_shape(int d, bool h_f32) {
+  if (d <= 256) return {256, 1, 3};
+  if (d <= kWarpRow) return {256, 3, 2};
+  auto threads = [d](int vpt) { return (ceil_div(d / 8, vpt) + 31) / 32 * 32; };
+  const int t1 = threads(1), t2 = threads(2);
+  if (!h_f32) return {t2, 2, std::max(1, 1024 / t2)};
+  if (d > 8192) return {threads(4), 4, std::max(1, 512 / threads(4))};
+  if (1024 / t1 * t1 >= 896) return {t1, 1, 1024 / t1};
+  return {t2, 2, std::max(1, 640 / t2)};
 }
-// CTAs of the backward: enough for two per SM, at most one per row group.
-inline int bwd_ctas(int64_t N, int d, int sms) {
-  const int g = bwd_groups(pick_config(d, N, 0));
-  const int64_t want = (N + g - 1) / g;
-  return (int)(want < 2 * (int64_t)sms ? want : 2 * (int64_t)sms);
+inline int bwd_ctas(int64_t N, int d, bool h_f32, int sms) {
+  const int rows = d <= kWarpRow ? 8 : 1;
+  return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * bwd_shape(d, h_f32).per_sm);
 }
 
 template <class DT, class HT>
 static moga_status launch_bwd(const BwdParams& p, int ctas, cudaStream_t s) {
-  switch (pick_config(p.d, p.N, 0)) {
-#define MOGA_NORM_CASE(I, TPR, VPT)                                                                         \
-  case I: {                                                                                                 \
-    constexpr int g = kCtaThreads<TPR> / TPR;                                                             \
-    const size_t smem = g > 1 ? (size_t)p.d * sizeof(float) : 0;                                            \
-    rms_norm_bwd_kernel<TPR, VPT, DT, HT><<<ctas, kCtaThreads<TPR>, smem, s>>>(p);                        \
-    break;                                                                                                  \
-  }
-    MOGA_NORM_CASE(0, 32, 3)
-    MOGA_NORM_CASE(1, 64, 3)
-    MOGA_NORM_CASE(2, 64, 5)
-    MOGA_NORM_CASE(3, 128, 5)
-    MOGA_NORM_CASE(4, 256, 5)
-    MOGA_NORM_CASE(5, 512, 5)
-#undef MOGA_NORM_CASE
+  const BwdShape k = bwd_shape(p.d, sizeof(HT) == 4);
+  const size_t smem = p.d * sizeof(float);
+  if (p.d <= 256) rms_norm_bwd_kernel<8, 1, DT, HT><<<ctas, k.threads, smem, s>>>(p);
+  else if (p.d <= kWarpRow) rms_norm_bwd_kernel<8, 3, DT, HT><<<ctas, k.threads, smem, s>>>(p);
+  else if (k.vpt == 2) rms_norm_bwd_kernel<1, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+  else if constexpr (sizeof(HT) == 4) {
+    if (k.vpt == 1) rms_norm_bwd_kernel<1, 1, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+    else rms_norm_bwd_kernel<1, 4, DT, HT><<<ctas, k.threads, 0, s>>>(p);
   }
   return check_launch("moga_rms_norm_bwd");
 }
@@ -492,7 +567,8 @@ extern "C" moga_status moga_rms_norm(const void* x, moga_dtype x_dt, const void*
 extern "C" size_t moga_rms_norm_bwd_ws_bytes(int64_t N, int32_t d) {
   using namespace moga::norm;
   if (N <= 0 || N > INT32_MAX / 2 || d <= 0 || d % 8 != 0 || d > kMaxD) return 0;
-  return (size_t)bwd_ctas(N, d, sm_count_of_current()) * d * sizeof(float);
+  const int sms = sm_count_of_current();
+  return (size_t)std::max(bwd_ctas(N, d, false, sms), bwd_ctas(N, d, true, sms)) * d * sizeof(float);
 }
 
 extern "C" moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const void* h, moga_dtype h_dt,
@@ -515,9 +591,9 @@ extern "C" moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const
                       reinterpret_cast<uintptr_t>(dx) | reinterpret_cast<uintptr_t>(dx_branch) |
                       reinterpret_cast<uintptr_t>(dw) | reinterpret_cast<uintptr_t>(ws);
   if (a & 15) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: pointers must be 16-byte aligned");
-  const int ctas = bwd_ctas(N, d, sm_count_of_current());
+  const int ctas = bwd_ctas(N, d, h_dt == MOGA_F32, sm_count_of_current());
   if (dw) {
-    const size_t need = (size_t)ctas * d * sizeof(float);
+    const size_t need = moga_rms_norm_bwd_ws_bytes(N, d);
     if (!ws) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: null workspace");
     if (ws_bytes < need)
       return fail(MOGA_ERR_WORKSPACE, "moga_rms_norm_bwd: workspace %zu < %zu bytes", ws_bytes, need);
