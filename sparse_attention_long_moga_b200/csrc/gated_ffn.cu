@@ -59,6 +59,13 @@ struct Tile {
   static_assert(kSmemBytes <= 227 * 1024 && kEnd < 32, "shared memory");
 };
 
+// dx or dW in the gradient launch
+struct Kind {
+  int units;                 // tiles x splits of K
+  int k, unit_k;             // k stages of a tile, of a unit
+  float* partial;            // fp32 sums [splits][rows][d] where K is split, else NULL
+};
+
 struct Params {
   int rows, cols;            // FWD, DGDU: N, F;  GRAD: N, d
   int n_k;                   // k stages of a forward tile
@@ -69,13 +76,12 @@ struct Params {
   const float *xs, *gs, *us; // e4m3 scales
   const __nv_bfloat16* dh;   // DGDU
   // GRAD
-  float* partial;            // [splits][2][F][d] where K is split, else NULL
   int F;
   int seg_k;                 // stages of the gate half of dx's K (F / 64 rounded up)
   int mf_tiles;              // row tiles of F
-  int n_dw, kc, kdw;         // dW units (tiles x splits), stages of one, stages of N
-  int n_dx;                  // dx tiles
-  int n1, a, b;              // dx tiles of the first n1 pairs (one dW unit more), of the others
+  Kind kind[2];              // dx, dW
+  int first;                 // the kind whose units each pair takes first
+  int n1, a, b;              // units of the other kind for the first n1 pairs, for the others
   long long timeout;
 };
 
@@ -96,11 +102,14 @@ __host__ __device__ __forceinline__ void tile_of(int t, int m_tiles, int n_tiles
   *m = b * kGroupM + (r - *n * gm);
 }
 
-// Gradient units.  dW tiles are few and long (K = N), dx tiles many and short
-// (K = 2F), and neither count fills the pairs' last round; together they do.
-// Each pair takes its dW units first (unit j P + pair), then dx tiles: the n1
-// pairs that have one dW unit more take `a` of them, the others `b`, with
-// b - a dx tiles about as long as a dW unit (plan_grad).
+// Gradient units.  dW's tiles are 2 F / 256 x d / 256 with K = N, dx's N / 256
+// x d / 256 with K = 2F: often few and long against many and short, and neither
+// count fills the pairs' last round.  So both kinds share one launch, K is
+// split where a tile would take longer than a pair's share of all the work
+// (grad_shape), and the longer units go first: unit j P + pair of the first
+// kind for each pair, then units of the other kind, of which the n1 pairs that
+// hold one more of the first take `a` and the others `b`, the difference being
+// about the length of one (plan_grad).
 // The j-th unit of pair `pair` of `P`; false when it has no more.
 template <int MODE>
 __host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int P, int j, Unit* u) {
@@ -114,26 +123,27 @@ __host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int 
     tile_of(t, p.m_tiles, p.n_tiles, &u->m, &u->n);
     return true;
   }
-  const int mine = p.n_dw / P + (pair < p.n_dw % P ? 1 : 0);
-  if (j < mine) {
-    const int t = j * P + pair, tiles = 2 * p.mf_tiles * p.n_tiles;
-    u->kind = 2;
-    u->split = t / tiles;
-    tile_of(t - u->split * tiles, 2 * p.mf_tiles, p.n_tiles, &u->m, &u->n);
-    u->up = u->m >= p.mf_tiles;
-    if (u->up) u->m -= p.mf_tiles;
-    u->k0 = u->split * p.kc;
-    u->k1 = u->k0 + p.kc < p.kdw ? u->k0 + p.kc : p.kdw;
-    return true;
+  const int n_first = p.kind[p.first].units;
+  const int mine = n_first / P + (pair < n_first % P ? 1 : 0);
+  int which = p.first, t = j * P + pair;
+  if (j >= mine) {
+    which ^= 1;
+    const int i = j - mine;
+    if (i >= (pair < p.n1 ? p.a : p.b)) return false;
+    t = i < p.a || p.n1 == 0 ? i * P + pair : p.a * P + (i - p.a) * (P - p.n1) + pair - p.n1;
+    if (t >= p.kind[which].units) return false;
   }
-  const int i = j - mine;
-  if (i >= (pair < p.n1 ? p.a : p.b)) return false;
-  const int t = i < p.a || p.n1 == 0 ? i * P + pair : p.a * P + (i - p.a) * (P - p.n1) + pair - p.n1;
-  if (t >= p.n_dx) return false;
-  u->kind = 1;
-  u->k0 = 0;
-  u->k1 = 2 * p.seg_k;
-  tile_of(t, p.m_tiles, p.n_tiles, &u->m, &u->n);
+  const Kind& kd = p.kind[which];
+  const int mt = which == 0 ? p.m_tiles : 2 * p.mf_tiles, tiles = mt * p.n_tiles;
+  u->kind = 1 + which;
+  u->split = t / tiles;
+  tile_of(t - u->split * tiles, mt, p.n_tiles, &u->m, &u->n);
+  if (which == 1 && u->m >= p.mf_tiles) {
+    u->up = 1;
+    u->m -= p.mf_tiles;
+  }
+  u->k0 = u->split * kd.unit_k;
+  u->k1 = u->k0 + kd.unit_k < kd.k ? u->k0 + kd.unit_k : kd.k;
   return true;
 }
 
@@ -338,6 +348,8 @@ template <int BN, int COLS>
 __device__ __forceinline__ void epilogue_grad(const Params& p, const CUtensorMap* map, const Unit& u, uint32_t acc,
                                               uint32_t box, int row0, int c_begin, int lane, uint32_t empty) {
   const int rows = u.kind == 1 ? p.rows : p.F;
+  float* const partial = p.kind[u.kind - 1].partial;
+  const bool split = partial != nullptr;
 #pragma unroll 1
   for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 64) {
     const int col = u.n * BN + c0;
@@ -345,7 +357,6 @@ __device__ __forceinline__ void epilogue_grad(const Params& p, const CUtensorMap
       release_acc(empty, lane);
       break;
     }
-    const bool split = u.kind == 2 && p.partial;
     if (!split) boxes_free<0>(lane);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -356,7 +367,8 @@ __device__ __forceinline__ void epilogue_grad(const Params& p, const CUtensorMap
       if (!split) {
         put32(box, lane, h, v);
       } else if (row0 + lane < rows) {
-        float* dst = p.partial + ((size_t)(u.split * 2 + u.up) * p.F + row0 + lane) * p.cols + col + 32 * h;
+        const size_t slab = u.kind == 1 ? u.split : u.split * 2 + u.up;
+        float* dst = partial + (slab * rows + row0 + lane) * p.cols + col + 32 * h;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (col + 32 * h + 4 * e < p.cols)
@@ -570,22 +582,31 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(2u * BN) : "memory");
 }
 
-// dW = bf16 of the sum of the K splits' partial sums, in split order;
-// n8 = F d / 8 groups of 8 values per matrix.
-__global__ void __launch_bounds__(256) ffn_dw_sum_kernel(const float* __restrict__ partial, int splits, int64_t n8,
-                                                         uint4* __restrict__ dwg, uint4* __restrict__ dwu) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= 2 * n8) return;
+// bf16 of the sum of the K splits' partial sums, in split order.  dx is N d / 8
+// groups of 8 values, dW_gate and dW_up F d / 8 each; a kind without partial
+// sums has no groups here.
+struct SumParams {
+  const float *px, *pw;
+  int sx, sw;
+  int64_t nx, nw;            // groups of dx, of one dW
+  uint4 *dx, *dwg, *dwu;
+};
+__global__ void __launch_bounds__(256) ffn_sum_kernel(const SumParams p) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const bool w = i >= p.nx;
+  if (w) i -= p.nx;
+  const int64_t n = w ? 2 * p.nw : p.nx;
+  if (i >= n) return;
+  const float4* q = reinterpret_cast<const float4*>(w ? p.pw : p.px) + 2 * i;
+  const int splits = w ? p.sw : p.sx;
   float v[8] = {};
-  for (int s = 0; s < splits; ++s) {
-    const float4* q = reinterpret_cast<const float4*>(partial) + ((size_t)s * 2 * n8 + i) * 2;
+  for (int s = 0; s < splits; ++s, q += 2 * n) {
     const float4 x = __ldcs(q), y = __ldcs(q + 1);
     v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
     v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
   }
-  const uint4 o = make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-  if (i < n8) dwg[i] = o;
-  else dwu[i - n8] = o;
+  (w ? i < p.nw ? p.dwg + i : p.dwu + (i - p.nw) : p.dx + i)[0] =
+      make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
 // ---------------------------------------------------------------- few tokens
@@ -638,7 +659,7 @@ struct FewParams {
 };
 
 template <bool E4M3, int ACT, int UN, int W>
-__global__ void __launch_bounds__(32 * W) ffn_few_kernel(const FewParams p) {
+__global__ void __launch_bounds__(32 * W, 1) ffn_few_kernel(const FewParams p) {
   __shared__ float red[W][4][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int f0 = blockIdx.x * 8;                      // F is a multiple of 8: all rows exist
@@ -788,49 +809,67 @@ static moga_status launch_gated(const Params& p, const void* x, const void* wg, 
 
 constexpr int kGradBN = 256;
 
-// Rows of a gradient tile in 256s: 512-row tiles read a quarter less operand
-// bytes per product, 256-row tiles give twice the units.  Depends on the sizes
-// alone, as the splits below, so the workspace does too.
-inline int grad_hm(int64_t N, int d, int F, int sms) {
-  const int64_t nt = ceil64(d, kGradBN);
-  return nt * (ceil64(N, 4 * BM) + 2 * ceil64(F, 4 * BM)) >= 3 * (int64_t)pair_count(sms) / 2 ? 2 : 1;
+// Tiles, units and splits of the gradient launch.  Depends on the sizes and
+// the SM count alone, not on the gradients asked for, so that the workspace
+// does too.
+struct GradShape {
+  int hm;                    // 512-row tiles (2) read a quarter less operand bytes per product; 256-row ones (1)
+                             // are twice as many: 512 where one and a half units per pair are left
+  int m_tiles, mf_tiles, n_tiles;
+  int tiles[2], k[2], unit_k[2], splits[2];   // dx, dW
+};
+inline GradShape grad_shape(int64_t N, int d, int F, int sms) {
+  GradShape g;
+  const int64_t P = pair_count(sms), nt = ceil64(d, kGradBN);
+  g.hm = 2 * nt * (ceil64(N, 4 * BM) + 2 * ceil64(F, 4 * BM)) >= 3 * P ? 2 : 1;
+  const int rows = 2 * g.hm * BM;
+  g.m_tiles = (int)ceil64(N, rows);
+  g.mf_tiles = ceil_div(F, rows);
+  g.n_tiles = (int)nt;
+  g.tiles[0] = g.m_tiles * g.n_tiles;
+  g.tiles[1] = 2 * g.mf_tiles * g.n_tiles;
+  g.k[0] = 2 * ceil_div(F, 64);
+  g.k[1] = (int)ceil64(N, 64);
+  // stages of a pair's share; below 8 a split's own cost exceeds what it saves
+  const int64_t share = ceil64((int64_t)g.tiles[0] * g.k[0] + (int64_t)g.tiles[1] * g.k[1], P);
+  const int least = (int)std::max<int64_t>(8, share);
+  for (int i = 0; i < 2; ++i) {
+    g.unit_k[i] = ceil_div(g.k[i], ceil_div(g.k[i], least));
+    g.splits[i] = ceil_div(g.k[i], g.unit_k[i]);
+  }
+  return g;
 }
-// Splits of dW's K: none where its tiles keep at least half of the pairs busy
-// (dx tiles fill the rest), else enough for about one unit per pair, of at
-// least 4 stages each.
-inline int dw_split_stages(int64_t N, int d, int F, int sms) {
-  const int P = pair_count(sms);
-  const int64_t tiles = 2 * ceil64(F, 2 * grad_hm(N, d, F, sms) * BM) * ceil64(d, kGradBN);
-  const int kdw = (int)ceil64(N, 64);
-  if (2 * tiles >= P) return kdw;
-  const int s = std::max(1, std::min((int)(P / tiles), kdw / 4));
-  return ceil_div(kdw, s);
+inline size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+inline size_t dgdu_bytes(int64_t N, int F) { return round256((size_t)2 * N * F * 2); }
+inline size_t dx_partial_bytes(const GradShape& g, int64_t N, int d) {
+  return g.splits[0] > 1 ? round256((size_t)g.splits[0] * N * d * sizeof(float)) : 0;
 }
-inline size_t dgdu_bytes(int64_t N, int F) { return ((size_t)2 * N * F * 2 + 255) / 256 * 256; }
-inline size_t grad_ws_bytes(int64_t N, int d, int F, int sms) {
-  const int splits = ceil_div((int)ceil64(N, 64), dw_split_stages(N, d, F, sms));
-  return dgdu_bytes(N, F) + (splits > 1 ? (size_t)splits * 2 * F * d * sizeof(float) : 0);
+inline size_t grad_ws_bytes(const GradShape& g, int64_t N, int d, int F) {
+  return dgdu_bytes(N, F) + dx_partial_bytes(g, N, d) +
+         (g.splits[1] > 1 ? (size_t)g.splits[1] * 2 * F * d * sizeof(float) : 0);
 }
 
 // The gradient units' shares (see unit_of).  Returns the number of pairs.
-inline int plan_grad(Params& p, int64_t N, int d, int F, bool need_dx, bool need_dw, int sms) {
+inline int plan_grad(Params& p, const GradShape& g, int64_t N, int d, int F, bool need_dx, bool need_dw, int sms) {
   p.rows = (int)N;
   p.cols = d;
   p.F = F;
-  const int rows = 2 * grad_hm(N, d, F, sms) * BM;
-  p.m_tiles = (int)ceil64(N, rows);
-  p.mf_tiles = ceil_div(F, rows);
-  p.n_tiles = ceil_div(d, kGradBN);
-  p.seg_k = ceil_div(F, 64);
-  p.kdw = (int)ceil64(N, 64);
-  p.kc = dw_split_stages(N, d, F, sms);
-  p.n_dw = need_dw ? 2 * p.mf_tiles * p.n_tiles * ceil_div(p.kdw, p.kc) : 0;
-  p.n_dx = need_dx ? p.m_tiles * p.n_tiles : 0;
-  const int P = (int)std::min<int64_t>((int64_t)p.n_dw + p.n_dx, pair_count(sms));
-  p.n1 = p.n_dw % P;
-  const int lag = ceil_div(p.kc, 2 * p.seg_k);   // dx tiles in the time of a dW unit
-  auto holds = [&](int b) { return (int64_t)p.n1 * std::max(0, b - lag) + (int64_t)(P - p.n1) * b >= p.n_dx; };
-  int lo = 0, hi = p.n_dx;
+  p.m_tiles = g.m_tiles;
+  p.mf_tiles = g.mf_tiles;
+  p.n_tiles = g.n_tiles;
+  p.seg_k = g.k[0] / 2;
+  for (int i = 0; i < 2; ++i) {
+    p.kind[i].units = (i == 0 ? need_dx : need_dw) ? g.tiles[i] * g.splits[i] : 0;
+    p.kind[i].k = g.k[i];
+    p.kind[i].unit_k = g.unit_k[i];
+  }
+  p.first = g.unit_k[1] >= g.unit_k[0] ? 1 : 0;
+  const Kind &one = p.kind[p.first], &two = p.kind[p.first ^ 1];
+  const int P = (int)std::min<int64_t>((int64_t)one.units + two.units, pair_count(sms));
+  p.n1 = one.units % P;
+  const int lag = ceil_div(one.unit_k, two.unit_k);   // units of the second kind in the time of one of the first
+  auto holds = [&](int b) { return (int64_t)p.n1 * std::max(0, b - lag) + (int64_t)(P - p.n1) * b >= two.units; };
+  int lo = 0, hi = two.units;
   while (lo < hi) {
     const int mid = lo + (hi - lo) / 2;
     if (holds(mid)) hi = mid;
@@ -895,7 +934,8 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
 extern "C" size_t moga_gated_ffn_bwd_ws_bytes(int64_t N, int32_t d, int32_t F) {
   if (N <= 0 || N > INT32_MAX / 2 || d <= 0 || d % 8 != 0 || F <= 0 || F % 8 != 0 || d > (1 << 20) || F > (1 << 20))
     return 0;
-  return moga::ffn::grad_ws_bytes(N, d, F, moga::route_tc::sm_count());
+  using namespace moga;
+  return ffn::grad_ws_bytes(ffn::grad_shape(N, d, F, route_tc::sm_count()), N, d, F);
 }
 
 extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, const void* w_up, int64_t N, int32_t d,
@@ -918,7 +958,8 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
                        reinterpret_cast<uintptr_t>(dw_up) | reinterpret_cast<uintptr_t>(ws);
   if (al & 15) return fail(MOGA_ERR_INVALID_ARG, "%s: pointers must be 16-byte aligned", who);
   const int sms = route_tc::sm_count();
-  const size_t need = grad_ws_bytes(N, d, F, sms);
+  const GradShape g = grad_shape(N, d, F, sms);
+  const size_t need = grad_ws_bytes(g, N, d, F);
   if (ws_bytes < need) return fail(MOGA_ERR_WORKSPACE, "%s: workspace %zu < %zu bytes", who, ws_bytes, need);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   __nv_bfloat16* dg = static_cast<__nv_bfloat16*>(ws);
@@ -930,9 +971,10 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
   p.cols = F;
   p.dh = static_cast<const __nv_bfloat16*>(dout);
   if ((st = launch_gated<MODE_DGDU, false>(p, x, w_gate, w_up, d, dg, du, who, s)) != MOGA_OK) return st;
-  const int pairs = plan_grad(p, N, d, F, dx != nullptr, dw_gate != nullptr, sms);
-  const int splits = ceil_div(p.kdw, p.kc);
-  p.partial = splits > 1 ? reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dgdu_bytes(N, F)) : nullptr;
+  const int pairs = plan_grad(p, g, N, d, F, dx != nullptr, dw_gate != nullptr, sms);
+  uint8_t* const part = static_cast<uint8_t*>(ws) + dgdu_bytes(N, F);
+  if (g.splits[0] > 1) p.kind[0].partial = reinterpret_cast<float*>(part);
+  if (g.splits[1] > 1) p.kind[1].partial = reinterpret_cast<float*>(part + dx_partial_bytes(g, N, d));
   ffn::Maps maps;
   const void* base[5] = {x, w_gate, w_up, dg, du};
   const int64_t rows[5] = {N, F, F, N, N}, cols[5] = {d, d, d, F, F};
@@ -943,16 +985,22 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
   const int64_t out_rows[3] = {dx ? N : F, dw_gate ? F : N, dw_up ? F : N};
   for (int i = 0; i < 3; ++i)
     if ((st = make_map(&maps.out[i], outs[i], out_rows[i], d, 2, 32)) != MOGA_OK) return st;
-  st = grad_hm(N, d, F, sms) == 2 ? launch<MODE_GRAD, false, 0, kGradBN, 2, 8>(p, maps, pairs, who, s)
-                                  : launch<MODE_GRAD, false, 0, kGradBN, 1, 8>(p, maps, pairs, who, s);
+  st = g.hm == 2 ? launch<MODE_GRAD, false, 0, kGradBN, 2, 8>(p, maps, pairs, who, s)
+                 : launch<MODE_GRAD, false, 0, kGradBN, 1, 8>(p, maps, pairs, who, s);
   if (st != MOGA_OK) return st;
-  if (dw_gate && splits > 1) {
-    const int64_t n8 = (int64_t)F * d / 8;
-    ffn_dw_sum_kernel<<<(unsigned)ceil64(2 * n8, 256), 256, 0, s>>>(p.partial, splits, n8, static_cast<uint4*>(dw_gate),
-                                                                   static_cast<uint4*>(dw_up));
-    return check_launch(who);
-  }
-  return MOGA_OK;
+  SumParams q = {};
+  if (dx && p.kind[0].partial) q.nx = N * d / 8;
+  if (dw_gate && p.kind[1].partial) q.nw = (int64_t)F * d / 8;
+  if (q.nx + q.nw == 0) return MOGA_OK;
+  q.px = p.kind[0].partial;
+  q.pw = p.kind[1].partial;
+  q.sx = g.splits[0];
+  q.sw = g.splits[1];
+  q.dx = static_cast<uint4*>(dx);
+  q.dwg = static_cast<uint4*>(dw_gate);
+  q.dwu = static_cast<uint4*>(dw_up);
+  ffn_sum_kernel<<<(unsigned)ceil64(q.nx + 2 * q.nw, 256), 256, 0, s>>>(q);
+  return check_launch(who);
 }
 
 // test hook (moga_testing.h): the units of every pair of one launch
@@ -963,7 +1011,7 @@ extern "C" int64_t moga_test_ffn_units(int32_t grad, int64_t N, int32_t d, int32
   ffn::Params p = {};
   int P;
   if (grad) {
-    P = plan_grad(p, N, d, F, need_dx != 0, need_dw != 0, sms);
+    P = plan_grad(p, grad_shape(N, d, F, sms), N, d, F, need_dx != 0, need_dw != 0, sms);
   } else {
     p.n_k = ceil_div(d, 64);
     p.m_tiles = (int)ceil64(N, 2 * ffn::BM);

@@ -87,7 +87,7 @@ def test_forward_e4m3(N, d, F, act, cuda_device):
                _np(wu.float()) * _np(us)[:, None], act)
 
 
-def _check_bwd(got, x, wg, wu, do, act):
+def _check_bwd(got, x, wg, wu, do, act, keys=("dx", "dw_gate", "dw_up")):
     N, F = do.shape
     g, u, eg, eu, a, da, ez = _parts(x, wg, wu, act)
     ref = block.gated_ffn_backward(x, wg, wu, do, act)
@@ -103,7 +103,7 @@ def _check_bwd(got, x, wg, wu, do, act):
         "dw_gate": edg.T @ np.abs(x) + (N / 16 + 6) * ULP * (ag.T @ np.abs(x)),
         "dw_up": edu.T @ np.abs(x) + (N / 16 + 6) * ULP * (au.T @ np.abs(x)),
     }
-    for k in ("dx", "dw_gate", "dw_up"):
+    for k in keys:
         out = _np(got[k])
         err = np.abs(out - ref[k])
         t = BF * np.abs(ref[k]) + 1.01 * tol[k] + 2.0 ** -126
@@ -163,7 +163,8 @@ def test_bad_token_stays_in_its_row(cuda_device):
 
 
 def test_offsets_past_32_bits(cuda_device):
-    """More than 2^31 outputs: the last rows equal a small call's with the same kernel (sizes above its own range)."""
+    """More than 2^31 outputs: the last rows equal a small call's; their gradients, whose K may be split differently
+    there, are the oracle's."""
     import torch
     import sparse_attention_long_moga_b200 as moga
     N, d, F = 270_000, 64, 8192
@@ -174,6 +175,6 @@ def test_offsets_past_32_bits(cuda_device):
     n = N % 512
     assert torch.equal(out[-n:], small[:n]) and torch.equal(out[:512], small)
     got = moga.moga_gated_ffn_backward(big, wg, wu, out, need_dw=False)
-    want = moga.moga_gated_ffn_backward(x, wg, wu, small, need_dw=False)
-    assert torch.equal(got["dx"][-n:], want["dx"][:n])
     moga.device_status()
+    for rows in (slice(N - n, N), slice(0, n)):
+        _check_bwd(dict(dx=got["dx"][rows]), _np(x[:n]), _np(wg), _np(wu), _np(small[:n]), "silu", keys=("dx",))
