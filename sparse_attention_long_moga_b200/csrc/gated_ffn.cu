@@ -42,16 +42,17 @@ constexpr int kHalfBox = 64 * kRowBytes;     // 8 KB: a box of 64 rows
 constexpr int kOutBox = 32 * kRowBytes;      // 4 KB: a warp's 32 rows x 64 bf16 columns of output
 constexpr int kGroupM = 8;                   // row tiles per band of the tile order
 
+// Shared memory of a CTA: operand stages, then the epilogue's output boxes.
 // Accumulators: HM = 1: 256 rows per pair, two buffers of BN columns;
 // HM = 2: 512 rows, the two accumulators hold a CTA's two halves of 128 rows.
-template <int BN, int HM>
+template <int BN, int HM, int BOXES = 8>
 struct Tile {
   static constexpr int kABytes = HM * BM * kRowBytes;     // this CTA's rows of A
   static constexpr int kBBytes = BN / 2 * kRowBytes;      // this CTA's half of the B rows
   static constexpr int kStageBytes = kABytes + kBBytes;
-  static constexpr int kStages = HM == 2 ? 4 : BN == 256 ? 6 : 8;
+  static constexpr int kStages = HM == 2 ? 4 : BN == 128 ? 8 : BOXES > 8 ? 5 : 6;
   static constexpr int kOutOff = kStages * kStageBytes;   // output boxes of the epilogue warps
-  static constexpr int kBarOff = kOutOff + 8 * kOutBox;
+  static constexpr int kBarOff = kOutOff + BOXES * kOutBox;
   static constexpr int kMiscOff = kBarOff + 32 * 8;
   static constexpr int kSmemBytes = kMiscOff + 64 + 1024;
   static constexpr int kFull = 0, kEmpty = kStages, kAccFull = 2 * kStages, kAccEmpty = kAccFull + 2,
@@ -294,25 +295,26 @@ __device__ __forceinline__ void load_dout(const Params& p, int row0, int col, in
   }
 }
 
-// dg and du of a gated tile's BN / 2 columns; v holds the first 64 columns of
-// dout (loaded before the products were waited for).
-template <int ACT, int BN>
+// dg and du of COLS columns of a gated tile from c_begin.  v holds the dout of
+// the first 64, loaded before the products were waited for; the next 64 are
+// loaded while these are worked on.  Box 0 takes dout, then dg, box 1 du.
+template <int ACT, int BN, int COLS>
 __device__ __forceinline__ void epilogue_dgdu(const Params& p, const CUtensorMap* mg, const CUtensorMap* mu,
-                                              uint32_t acc, uint32_t boxes, int row0, int col0, int lane, uint4* v,
-                                              uint32_t empty) {
+                                              uint32_t acc, uint32_t boxes, int row0, int col0, int c_begin, int lane,
+                                              uint4* v, uint32_t empty) {
 #pragma unroll 1
-  for (int c0 = 0; c0 < BN / 2; c0 += 64) {
+  for (int c0 = c_begin; c0 < c_begin + COLS; c0 += 64) {
     const int col = col0 + c0;
     if (col >= p.cols || row0 >= p.rows) {   // the whole warp
       release_acc(empty, lane);
       break;
     }
-    if (c0 > 0) load_dout(p, row0, col, lane, v);
     boxes_free<0>(lane);
-    // dout from lanes of columns to lanes of rows, through the first box
+    // dout from lanes of columns to lanes of rows
 #pragma unroll
     for (int i = 0; i < 8; ++i) sts16(box_addr(boxes, 4 * i + (lane >> 3), lane & 7), v[i]);
     __syncwarp();
+    if (c0 + 64 < c_begin + COLS) load_dout(p, row0, col + 64, lane, v);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t w[16];
@@ -325,7 +327,7 @@ __device__ __forceinline__ void epilogue_dgdu(const Params& p, const CUtensorMap
       tmem_ld32(acc + c0 + 32 * h, g);
       tmem_ld32(acc + BN / 2 + c0 + 32 * h, u);
       tmem_wait_ld();
-      if (h == 1 && c0 + 64 >= BN / 2) release_acc(empty, lane);
+      if (h == 1 && c0 + 64 >= c_begin + COLS) release_acc(empty, lane);
 #pragma unroll
       for (int j = 0; j < 32; ++j) {
         const float d = __uint_as_float((j & 1) ? (w[j >> 1] & 0xffff0000u) : (w[j >> 1] << 16));
@@ -387,10 +389,14 @@ struct Maps {
   CUtensorMap m[5], out[3];
 };
 
+// output boxes of a CTA: two per warp for dg and du, else eight to share
+__host__ __device__ constexpr int boxes_of(int mode, int ew) { return mode == MODE_DGDU ? 2 * ew : 8; }
+
 template <int MODE, bool E4M3, int ACT, int BN, int HM, int EW>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__((EW + 2) * 32, 1)
 ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
-  using T = Tile<BN, HM>;
+  constexpr int kBoxes = boxes_of(MODE, EW);
+  using T = Tile<BN, HM, kBoxes>;
   constexpr int BK = E4M3 ? 128 : 64;
   // instruction descriptors of a pair's M = 256 product
   constexpr uint32_t kIdesc = pair_desc(instr_desc(BN, false));
@@ -542,7 +548,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
     // ------------------------------------------------------------------ epilogue
     const int quarter = warp & 3, half = warp >> 2;
     const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-    const uint32_t boxes = sbase + T::kOutOff + warp * (8 / EW) * kOutBox;   // this warp's boxes
+    const uint32_t boxes = sbase + T::kOutOff + warp * (kBoxes / EW) * kOutBox;   // this warp's boxes
     int turn = 0;
     Unit u;
     for (int j = 0; unit_of<MODE>(p, pair, n_pairs, j, &u); ++j) {
@@ -550,7 +556,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
       const uint32_t parity = HM == 1 ? (j >> 1) & 1 : j & 1;
       const int row0 = (u.m * 2 + (int)rank) * HM * BM + quarter * 32;
       uint4 v[MODE == MODE_DGDU ? 8 : 1];
-      if (MODE == MODE_DGDU) load_dout(p, row0, u.n * (BN / 2), lane, v);
+      if (MODE == MODE_DGDU) load_dout(p, row0, u.n * (BN / 2) + half * (BN * 2 / EW), lane, v);
       if (!__all_sync(0xffffffffu, mbar_wait(bar(T::kAccFull + b), parity, abort_flag, p.timeout))) break;
       tc_fence_after();
 #pragma unroll 1
@@ -561,8 +567,8 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
           epilogue_fwd<E4M3, ACT, BN, BN * 2 / EW, 8 / EW>(p, &maps.out[0], acc, boxes, row0, u.n * (BN / 2),
                                                            half * (BN * 2 / EW), lane, turn, empty);
         else if constexpr (MODE == MODE_DGDU)
-          epilogue_dgdu<ACT, BN>(p, &maps.out[0], &maps.out[1], acc, boxes, row0, u.n * (BN / 2), lane, v,
-                                 empty);
+          epilogue_dgdu<ACT, BN, BN * 2 / EW>(p, &maps.out[0], &maps.out[1], acc, boxes, row0, u.n * (BN / 2),
+                                              half * (BN * 2 / EW), lane, v, empty);
         else
           epilogue_grad<BN, BN * 4 / EW>(p, &maps.out[u.kind == 1 ? 0 : 1 + u.up], u, acc, boxes, row0 + h * BM,
                                          half * (BN * 4 / EW), lane, empty);
@@ -611,22 +617,32 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const SumParams p) {
 
 // ---------------------------------------------------------------- few tokens
 //
-// Up to kFewTokens tokens the weights' read is the time (2 F d elements for
-// N d + N F others), and a 256-row tile would idle.  A CTA takes 8 columns of
-// F and all tokens; its W warps split d, each streaming 64-byte pieces of 16
-// weight rows straight from global memory into mma.sync fragments: the 16-row
-// A tile is 8 gate rows over the 8 up rows of the same columns, so a lane's
+// For few tokens the weights' read is the time (2 F d elements for N d + N F
+// others), a 256-row tile would idle, and a tile's k stages follow one another
+// at 300 ns each however narrow it is.  Here a CTA takes 8 columns of F and
+// all tokens; its W warps split d, each streaming 64-byte pieces of 16 weight
+// rows straight from global memory into mma.sync fragments: the 16-row A tile
+// is 8 gate rows over the 8 up rows of the same columns, so a lane's
 // accumulators hold gate and up of the same outputs.  A lane loads 16
 // consecutive bytes of a row where the fragment wants four pieces spread over
 // k; the sum over k does not mind the order as long as x is read in the same
 // one.  No shared-memory stage, no barrier in the loop: a lane keeps 2 UN
-// 16-byte loads under way, and many small CTAs per SM do the rest (UN = 4,
-// W = 8 in bf16, UN = 8, W = 4 in e4m3: the fewest registers that hold the
-// loads of one pass over d = 1536 to 5120; twice the unrolling measured 47
-// instead of 43.5 us, half the warps 46).  One token through 5120 x 13824:
-// 43.5 us, the weights at the copy rate (6.5 TB/s); e4m3 27 us, 5.2 TB/s.
-// The warps' sums meet in shared memory in a fixed order.
-constexpr int kFewTokens = 8;
+// 16-byte loads of weights under way, and many small CTAs per SM do the rest
+// (up to 8 tokens UN = 4, W = 8 in bf16, UN = 8, W = 4 in e4m3; twice the
+// unrolling measured 47 instead of 43.5 us, half the warps 46; one block per
+// SM as the launch bound lets the loads of a pass stay in registers, 45.8
+// against 50 us).  The warps' sums meet in shared memory in a fixed order.
+// One token through 5120 x 13824: 44.5 us, the weights at 6.4 TB/s.
+
+// Up to 16 tokens this kernel is always the faster (16 tokens, 5120 x 13824:
+// 52 against 64 us; 1536 x 4096: 8.3 against 13.1).  Above, every CTA's read of
+// x costs as much as its weights, so it pays while the CTAs are few: 32 tokens
+// up to three per SM (5120 x 2048: 19 against 30 us, 1536 x 4096: 14.2 against
+// 13.2), 64 tokens up to one (2048 x 1024: 8.5 against 14.9, 2048 x 2048: 15.8
+// against 15.3).
+inline bool few_tokens(int64_t N, int F, int sms) {
+  return N <= 16 || (N <= 32 && F / 8 <= 3 * sms) || (N <= 64 && F / 8 <= sms);
+}
 
 __device__ __forceinline__ uint4 ldg_stream(const void* p) {
   uint4 v;
@@ -658,20 +674,27 @@ struct FewParams {
   __nv_bfloat16* out;
 };
 
-template <bool E4M3, int ACT, int UN, int W>
+template <bool E4M3, int ACT, int NT, int UN, int W>
 __global__ void __launch_bounds__(32 * W, 1) ffn_few_kernel(const FewParams p) {
-  __shared__ float red[W][4][32];
+  __shared__ float red[W][4 * NT][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
   const int f0 = blockIdx.x * 8;                      // F is a multiple of 8: all rows exist
   const uint8_t* wg = p.wg + (size_t)(f0 + g) * p.row_bytes + 16 * q;
   const uint8_t* wu = p.wu + (size_t)(f0 + g) * p.row_bytes + 16 * q;
-  const bool xon = g < p.N;
-  const uint8_t* xp = p.x + (size_t)(xon ? g : 0) * p.row_bytes + 16 * q;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f};
+  bool xon[NT];
+  const uint8_t* xp[NT];
+  float acc[NT][4];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    xon[n] = 8 * n + g < p.N;
+    xp[n] = p.x + (size_t)(xon[n] ? 8 * n + g : 0) * p.row_bytes + 16 * q;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+  }
   const uint4 zero = make_uint4(0, 0, 0, 0);
   // step s covers bytes [64 s, 64 s + 64) of every row; warp w takes s = w, w + W, ...
   for (int s0 = warp; 64 * s0 < p.row_bytes; s0 += W * UN) {
-    uint4 a[UN], b[UN], x[UN];
+    uint4 a[UN], b[UN], x[UN][NT];
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       const int k = 64 * (s0 + W * i);
@@ -682,39 +705,49 @@ __global__ void __launch_bounds__(32 * W, 1) ffn_few_kernel(const FewParams p) {
 #pragma unroll
     for (int i = 0; i < UN; ++i) {
       const int k = 64 * (s0 + W * i);
-      x[i] = xon && k + 16 * q < p.row_bytes ? __ldg(reinterpret_cast<const uint4*>(xp + k)) : zero;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        x[i][n] = xon[n] && k + 16 * q < p.row_bytes ? __ldg(reinterpret_cast<const uint4*>(xp[n] + k)) : zero;
     }
 #pragma unroll
-    for (int i = 0; i < UN; ++i) {
-      mma_16x8<E4M3>(acc, a[i].x, b[i].x, a[i].y, b[i].y, x[i].x, x[i].y);
-      mma_16x8<E4M3>(acc, a[i].z, b[i].z, a[i].w, b[i].w, x[i].z, x[i].w);
-    }
+    for (int i = 0; i < UN; ++i)
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        mma_16x8<E4M3>(acc[n], a[i].x, b[i].x, a[i].y, b[i].y, x[i][n].x, x[i][n].y);
+        mma_16x8<E4M3>(acc[n], a[i].z, b[i].z, a[i].w, b[i].w, x[i][n].z, x[i][n].w);
+      }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) red[warp][i][lane] = acc[i];
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) red[warp][4 * n + i][lane] = acc[n][i];
   __syncthreads();
-  // column c, token t: lane 4 c + t / 2, slot t % 2 (gate), 2 + t % 2 (up)
-  const int c = threadIdx.x & 7, t = threadIdx.x >> 3;
-  if (t >= p.N) return;
-  const int l = 4 * c + (t >> 1), slot = t & 1;
-  float gate = 0.f, up = 0.f;
+  // column c, token t: lane 4 c + (t % 8) / 2, slot 4 (t / 8) + t % 2 (gate), 2 more (up)
+  for (int o = threadIdx.x; o < 8 * p.N; o += 32 * W) {
+    const int c = o & 7, t = o >> 3, l = 4 * c + ((t & 7) >> 1), slot = 4 * (t >> 3) + (t & 1);
+    float gate = 0.f, up = 0.f;
 #pragma unroll
-  for (int w = 0; w < W; ++w) {
-    gate += red[w][slot][l];
-    up += red[w][slot + 2][l];
+    for (int w = 0; w < W; ++w) {
+      gate += red[w][slot][l];
+      up += red[w][slot + 2][l];
+    }
+    if (E4M3) {
+      const float xs = __ldg(p.xs + t);
+      gate *= xs * __ldg(p.gs + f0 + c);
+      up *= xs * __ldg(p.us + f0 + c);
+    }
+    p.out[(size_t)t * p.F + f0 + c] = __float2bfloat16_rn(act_of<ACT>(gate) * up);
   }
-  if (E4M3) {
-    const float xs = __ldg(p.xs + t);
-    gate *= xs * __ldg(p.gs + f0 + c);
-    up *= xs * __ldg(p.us + f0 + c);
-  }
-  p.out[(size_t)t * p.F + f0 + c] = __float2bfloat16_rn(act_of<ACT>(gate) * up);
 }
 
 template <bool E4M3, int ACT>
 static moga_status launch_few(const FewParams& p, const char* who, cudaStream_t s) {
   constexpr int UN = E4M3 ? 8 : 4, W = E4M3 ? 4 : 8;
-  ffn_few_kernel<E4M3, ACT, UN, W><<<p.F / 8, 32 * W, 0, s>>>(p);
+  const int grid = p.F / 8;
+  if (p.N <= 8) ffn_few_kernel<E4M3, ACT, 1, UN, W><<<grid, 32 * W, 0, s>>>(p);
+  else if (p.N <= 16) ffn_few_kernel<E4M3, ACT, 2, 4, 8><<<grid, 256, 0, s>>>(p);
+  else if (p.N <= 32) ffn_few_kernel<E4M3, ACT, 4, 2, 8><<<grid, 256, 0, s>>>(p);
+  else ffn_few_kernel<E4M3, ACT, 8, 1, 8><<<grid, 256, 0, s>>>(p);
   return check_launch(who);
 }
 
@@ -737,9 +770,9 @@ static moga_status make_map(CUtensorMap* m, const void* base, int64_t rows, int6
 template <int MODE, bool E4M3, int ACT, int BN, int HM, int EW>
 static moga_status launch(const Params& p, const Maps& maps, int pairs, const char* who, cudaStream_t s) {
   auto* k = ffn_kernel<MODE, E4M3, ACT, BN, HM, EW>;
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN, HM>::kSmemBytes);
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN, HM, boxes_of(MODE, EW)>::kSmemBytes);
   if (e != cudaSuccess) return fail(MOGA_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
-  k<<<2 * pairs, (EW + 2) * 32, Tile<BN, HM>::kSmemBytes, s>>>(p, maps);
+  k<<<2 * pairs, (EW + 2) * 32, Tile<BN, HM, boxes_of(MODE, EW)>::kSmemBytes, s>>>(p, maps);
   return check_launch(who);
 }
 
@@ -781,9 +814,14 @@ static moga_status launch_gated_bn(Params p, const void* x, const void* wg, cons
   p.n_tiles = ceil_div(p.cols, BN / 2);
   p.total = p.m_tiles * p.n_tiles;
   const int pairs = std::min(p.total, pair_count(sms));
-  // Warps of the epilogue: eight, with half of the columns each, where a half
-  // is a box wide and a warp needs only one.
-  constexpr int EW = MODE == MODE_FWD && BN == 256 ? 8 : 4;
+  // Epilogue warps: eight, one for each 64 columns of the tile's rows.  For dg
+  // and du, whose 16 boxes then cost an operand stage, only where the epilogue
+  // is longer than the products (16,384 tokens, F = 1024: d = 512 40.6 against
+  // 41.6 us with four, d = 768 52.3 against 46.9).
+  if (BN == 256 && (MODE == MODE_FWD || p.n_k <= 8))
+    return p.act == MOGA_ACT_SILU ? launch<MODE, E4M3, MOGA_ACT_SILU, BN, 1, BN / 32>(p, maps, pairs, who, s)
+                                  : launch<MODE, E4M3, MOGA_ACT_GELU, BN, 1, BN / 32>(p, maps, pairs, who, s);
+  constexpr int EW = 4;
   return p.act == MOGA_ACT_SILU ? launch<MODE, E4M3, MOGA_ACT_SILU, BN, 1, EW>(p, maps, pairs, who, s)
                                 : launch<MODE, E4M3, MOGA_ACT_GELU, BN, 1, EW>(p, maps, pairs, who, s);
 }
@@ -903,7 +941,7 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
   if (((a | ws) & 15) || (reinterpret_cast<uintptr_t>(x_scale) & 3))
     return fail(MOGA_ERR_INVALID_ARG, "%s: x, w_gate, w_up, their scales and out must be 16-byte aligned", who);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (N <= kFewTokens) {
+  if (few_tokens(N, F, route_tc::sm_count())) {
     FewParams q = {};
     q.x = static_cast<const uint8_t*>(x);
     q.wg = static_cast<const uint8_t*>(w_gate);
