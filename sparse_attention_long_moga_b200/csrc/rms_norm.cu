@@ -235,10 +235,10 @@ rms_norm_kernel(const FwdParams p) {
       load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float t = f[i][j] * w[j], e = fmaf(f[i][j], w[j], -t);
+        const float t = f[i][j] * w[j], e = fmaf(fabsf(f[i][j]), fabsf(w[j]), -fabsf(t));
         if (fabsf(t) > mx) {
           mx = fabsf(t);
-          me = t < 0.f ? -e : e;
+          me = e;
         }
         f[i][j] = t;
       }
@@ -260,7 +260,7 @@ rms_norm_kernel(const FwdParams p) {
       for (int j = 0; j < 8; ++j) {
         q[j] = (f[i][j] * k1) * k2;
         // within 8 units of a tie of the 3-bit mantissa; the four roundings above are worth 4 at most
-        near |= ((__float_as_uint(q[j]) + 8u) & 0xfffffu) - 0x80000u <= 16u;
+        near |= (__float_as_uint(q[j]) << 12) - ((0x80000u - 8u) << 12) <= 16u << 12;
       }
       if (near && direct) {   // 1 vector in 8000
         const float k2lo = (fmaf(-k2, mx, kE4m3Max) - k2 * me) / mx;
