@@ -484,7 +484,8 @@ moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const void* h, m
  *               moga_rms_norm writes them); NULL with MOGA_BF16
  * act:          MOGA_ACT_SILU or MOGA_ACT_GELU
  * out:          [N][F] bf16, written
- * Requires d % 8 == 0 (e4m3: d % 16 == 0), F % 8 == 0, d, F <= 2^20, N < 2^30
+ * Requires d % 8 == 0 (e4m3: d % 16 == 0), F % 8 == 0, d, F <= 2^20, N < 2^30,
+ * N * max(d, F) < 2^44
  * and 16-byte aligned x, w_gate, w_up, their scales and out.  Needs no
  * workspace. */
 moga_status moga_gated_ffn(const void* x, const void* w_gate, const void* w_up, moga_dtype dt,
@@ -497,8 +498,10 @@ moga_status moga_gated_ffn(const void* x, const void* w_gate, const void* w_up, 
  *   dx = dg . W_gate + du . W_up,   dW_gate = dg^T . x,   dW_up = du^T . x
  * dout: [N][F] bf16;  dx: [N][d] bf16, written, or NULL to skip;
  * dw_gate, dw_up: [F][d] bf16, written, or both NULL to skip
- * ws:   moga_gated_ffn_bwd_ws_bytes(N, d, F) bytes, 16-byte aligned (dg and
- *       du).  Returns 0 for arguments the call would reject.
+ * ws:   moga_gated_ffn_bwd_ws_bytes(N, d, F) bytes, 16-byte aligned: dg and du
+ *       (4 N F bytes), and fp32 partial sums where the sizes give too few
+ *       tiles to fill the GPU and K is split.  Returns 0 for arguments the
+ *       call would reject.  Deterministic: every sum runs in a fixed order.
  * Limits as for the bf16 forward. */
 size_t moga_gated_ffn_bwd_ws_bytes(int64_t N, int32_t d, int32_t F);
 moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, const void* w_up, int64_t N, int32_t d,

@@ -781,14 +781,18 @@ inline int64_t ceil64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // one pair of CTAs per pair of SMs (persistent)
 inline int pair_count(int sms) { return sms / 2 > 0 ? sms / 2 : 1; }
 
+// tile counts stay below 2^30
+inline bool sizes_ok(int64_t N, int64_t d, int64_t F) {
+  return d <= (1 << 20) && F <= (1 << 20) && ceil64(N, 256) * ceil64(std::max(d, F), 64) <= INT32_MAX / 2;
+}
+
 static moga_status check_dims(const char* who, int64_t N, int32_t d, int32_t F, int32_t act, int elem) {
   const int m = 16 / elem;   // 16-byte rows, as the TMA copies need them
   if (N <= 0 || N > INT32_MAX / 2) return fail(MOGA_ERR_INVALID_ARG, "%s: N=%lld out of range", who, (long long)N);
   if (d <= 0 || d % m != 0)
     return fail(MOGA_ERR_INVALID_ARG, "%s: d=%d must be a positive multiple of %d", who, d, m);
   if (F <= 0 || F % 8 != 0) return fail(MOGA_ERR_INVALID_ARG, "%s: F=%d must be a positive multiple of 8", who, F);
-  if (d > (1 << 20) || F > (1 << 20) || ceil64(N, 256) * ceil64(F, 32) > INT32_MAX / 2)
-    return fail(MOGA_ERR_INVALID_ARG, "%s: sizes out of range", who);
+  if (!sizes_ok(N, d, F)) return fail(MOGA_ERR_INVALID_ARG, "%s: sizes out of range", who);
   if (act != MOGA_ACT_SILU && act != MOGA_ACT_GELU)
     return fail(MOGA_ERR_INVALID_ARG, "%s: activation %d unknown", who, act);
   return MOGA_OK;
@@ -927,14 +931,14 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
   using namespace moga;
   using namespace moga::ffn;
   const char* who = "moga_gated_ffn";
-  if (!x || !w_gate || !w_up || !out) return fail(MOGA_ERR_INVALID_ARG, "%s: null pointer", who);
   if (dt != MOGA_BF16 && dt != MOGA_E4M3) return fail(MOGA_ERR_INVALID_ARG, "%s: dtype must be bf16 or e4m3", who);
   const bool f8 = dt == MOGA_E4M3;
-  if (f8 != (x_scale != nullptr) || f8 != (w_gate_scale != nullptr) || f8 != (w_up_scale != nullptr))
-    return fail(MOGA_ERR_INVALID_ARG, "%s: the three scales go with e4m3 operands", who);
   const int elem = f8 ? 1 : 2;
   moga_status st = check_dims(who, N, d, F, act, elem);
   if (st != MOGA_OK) return st;
+  if (!x || !w_gate || !w_up || !out) return fail(MOGA_ERR_INVALID_ARG, "%s: null pointer", who);
+  if (f8 != (x_scale != nullptr) || f8 != (w_gate_scale != nullptr) || f8 != (w_up_scale != nullptr))
+    return fail(MOGA_ERR_INVALID_ARG, "%s: the three scales go with e4m3 operands", who);
   const uintptr_t a = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_gate) |
                       reinterpret_cast<uintptr_t>(w_up) | reinterpret_cast<uintptr_t>(out);
   const uintptr_t ws = reinterpret_cast<uintptr_t>(w_gate_scale) | reinterpret_cast<uintptr_t>(w_up_scale);
@@ -970,9 +974,8 @@ extern "C" moga_status moga_gated_ffn(const void* x, const void* w_gate, const v
 }
 
 extern "C" size_t moga_gated_ffn_bwd_ws_bytes(int64_t N, int32_t d, int32_t F) {
-  if (N <= 0 || N > INT32_MAX / 2 || d <= 0 || d % 8 != 0 || F <= 0 || F % 8 != 0 || d > (1 << 20) || F > (1 << 20))
-    return 0;
   using namespace moga;
+  if (N <= 0 || N > INT32_MAX / 2 || d <= 0 || d % 8 != 0 || F <= 0 || F % 8 != 0 || !ffn::sizes_ok(N, d, F)) return 0;
   return ffn::grad_ws_bytes(ffn::grad_shape(N, d, F, route_tc::sm_count()), N, d, F);
 }
 
@@ -982,14 +985,12 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
   using namespace moga;
   using namespace moga::ffn;
   const char* who = "moga_gated_ffn_bwd";
+  moga_status st = check_dims(who, N, d, F, act, 2);
+  if (st != MOGA_OK) return st;
   if (!x || !w_gate || !w_up || !dout || !ws) return fail(MOGA_ERR_INVALID_ARG, "%s: null pointer", who);
   if ((dw_gate != nullptr) != (dw_up != nullptr))
     return fail(MOGA_ERR_INVALID_ARG, "%s: dw_gate and dw_up go together", who);
   if (!dx && !dw_gate) return fail(MOGA_ERR_INVALID_ARG, "%s: no gradient asked for", who);
-  moga_status st = check_dims(who, N, d, F, act, 2);
-  if (st != MOGA_OK) return st;
-  if (ceil64(N, 256) * ceil64(d, 256) > INT32_MAX / 2)
-    return fail(MOGA_ERR_INVALID_ARG, "%s: sizes out of range", who);
   const uintptr_t al = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w_gate) |
                        reinterpret_cast<uintptr_t>(w_up) | reinterpret_cast<uintptr_t>(dout) |
                        reinterpret_cast<uintptr_t>(dx) | reinterpret_cast<uintptr_t>(dw_gate) |

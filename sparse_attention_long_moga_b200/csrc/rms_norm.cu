@@ -529,6 +529,8 @@ extern "C" moga_status moga_rms_norm(const void* x, moga_dtype x_dt, const void*
                                      void* y, moga_dtype y_dt, float* scale, void* stream) {
   using namespace moga;
   using namespace moga::norm;
+  moga_status st = check_dims("moga_rms_norm", N, d, eps);
+  if (st != MOGA_OK) return st;
   if (!x || !w || !y) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: null pointer");
   if ((residual != nullptr) != (h != nullptr))
     return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: residual and h go together");
@@ -537,8 +539,6 @@ extern "C" moga_status moga_rms_norm(const void* x, moga_dtype x_dt, const void*
     return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: bad dtype");
   if ((y_dt == MOGA_E4M3) != (scale != nullptr))
     return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm: scale goes with an e4m3 output");
-  moga_status st = check_dims("moga_rms_norm", N, d, eps);
-  if (st != MOGA_OK) return st;
   if (residual && x_dt == MOGA_F32 && res_dt == MOGA_BF16)
     return fail(MOGA_ERR_UNSUPPORTED, "moga_rms_norm: an fp32 x needs an fp32 residual");
   const uintptr_t a = reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(residual) |
@@ -577,11 +577,11 @@ extern "C" moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const
                                          void* stream) {
   using namespace moga;
   using namespace moga::norm;
+  moga_status st = check_dims("moga_rms_norm_bwd", N, d, eps);
+  if (st != MOGA_OK) return st;
   if (!dy || !h || !w || !dx) return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: null pointer");
   if (!is_float_dt(dy_dt) || !is_float_dt(h_dt) || !is_float_dt(w_dt))
     return fail(MOGA_ERR_INVALID_ARG, "moga_rms_norm_bwd: bad dtype");
-  moga_status st = check_dims("moga_rms_norm_bwd", N, d, eps);
-  if (st != MOGA_OK) return st;
   if (dy_dt == MOGA_F32 && h_dt == MOGA_BF16)
     return fail(MOGA_ERR_UNSUPPORTED, "moga_rms_norm_bwd: an fp32 dy needs an fp32 h");
   if (dx_branch && h_dt == MOGA_BF16)

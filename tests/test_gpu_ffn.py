@@ -1,23 +1,11 @@
-"""GPU parity of the gated feed-forward (bf16 and e4m3) and of its backward against the fp64 oracle.
-
-Tolerances, per element.  The tensor core adds K = 16 (bf16) or 32 (e4m3)
-products a step into an fp32 accumulator and truncates: one unit, 2^-23, of
-the partial sum a step, so a projection is off by E(g) = (d / 16) 2^-23
-sum_k |x_k w_k| at most (as for the Q/K/V projection).  exp and the quotient
-of the activation are off by (16 + 8 |z|) 2^-23 relative, z the sigmoid's
-argument.  The result is rounded to bf16: 2^-8.  In the backward dg and du
-carry those errors and one bf16 rounding each, which the products that follow
-carry over term by term, adding their own accumulation and rounding.
-"""
-import numpy as np
+"""GPU parity of the gated feed-forward (bf16 and e4m3) and of its backward against the fp64 oracle (tolerances:
+_block.py)."""
 import pytest
 
-from oracle import block
+from _block import check_ffn, check_ffn_backward
+from _block import to_np as _np
 
 pytestmark = pytest.mark.gpu
-
-BF = 2.0 ** -8
-ULP = 2.0 ** -23
 
 SHAPES = [(1, 16, 8), (1, 64, 128), (1, 1536, 264), (2, 80, 136), (7, 528, 96), (8, 128, 16), (9, 256, 520),
           (16, 1536, 512), (17, 144, 360), (31, 2048, 128), (32, 96, 1032), (33, 512, 256), (64, 1536, 384),
@@ -39,30 +27,6 @@ def _inputs(torch, dev, N, d, F, seed, e4m3=False):
     return out, do
 
 
-def _np(t):
-    return t.double().cpu().numpy()
-
-
-def _parts(x, wg, wu, act):
-    """g, u, their accumulation errors, act, act' and the activation's own relative error."""
-    d = x.shape[1]
-    g, u = x @ wg.T, x @ wu.T
-    eg, eu = ((d / 16 + 4) * ULP * (np.abs(x) @ np.abs(w).T) for w in (wg, wu))
-    a, da = block.activation(g, act)
-    z = np.abs(g) if act == "silu" else 1.6 * (np.abs(g) + 0.045 * np.abs(g) ** 3)
-    return g, u, eg, eu, a, da, (16 + 8 * z) * ULP
-
-
-def _check_fwd(out, x, wg, wu, act):
-    g, u, eg, eu, a, da, ez = _parts(x, wg, wu, act)
-    want = a * u
-    # |act'| over the error's reach: at most |act'(g)| + 1.2 E(g)
-    slack = (np.abs(da) + 1.2 * eg) * eg * (np.abs(u) + eu) + np.abs(a) * eu + ez * np.abs(want)
-    err = np.abs(out - want)
-    tol = BF * np.abs(want) + 1.01 * slack + 2.0 ** -126
-    assert np.all(err <= tol), "worst error / tolerance %.3f" % np.max(err / tol)
-
-
 @pytest.mark.parametrize("act", ["silu", "gelu"])
 @pytest.mark.parametrize("N,d,F", SHAPES)
 def test_forward_bf16(N, d, F, act, cuda_device):
@@ -72,7 +36,7 @@ def test_forward_bf16(N, d, F, act, cuda_device):
     out = moga.moga_gated_ffn(x, wg, wu, act=act)
     moga.device_status()
     assert out.dtype == torch.bfloat16 and out.shape == (N, F)
-    _check_fwd(_np(out), _np(x), _np(wg), _np(wu), act)
+    check_ffn(_np(out), _np(x), _np(wg), _np(wu), act)
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -83,33 +47,8 @@ def test_forward_e4m3(N, d, F, act, cuda_device):
     ((x, xs), (wg, gs), (wu, us)), _ = _inputs(torch, cuda_device, N, d, F, N + d + F, e4m3=True)
     out = moga.moga_gated_ffn(x, wg, wu, act=act, x_scale=xs, w_gate_scale=gs, w_up_scale=us)
     moga.device_status()
-    _check_fwd(_np(out), _np(x.float()) * _np(xs)[:, None], _np(wg.float()) * _np(gs)[:, None],
+    check_ffn(_np(out), _np(x.float()) * _np(xs)[:, None], _np(wg.float()) * _np(gs)[:, None],
                _np(wu.float()) * _np(us)[:, None], act)
-
-
-def _check_bwd(got, x, wg, wu, do, act, keys=("dx", "dw_gate", "dw_up")):
-    N, F = do.shape
-    g, u, eg, eu, a, da, ez = _parts(x, wg, wu, act)
-    ref = block.gated_ffn_backward(x, wg, wu, do, act)
-    # errors of the stored dg and du
-    dda = 1.2 * eg + ez * (1 + np.abs(a) + np.abs(da) + (0 if act == "silu" else 2 * np.abs(a) * (1 + 0.14 * g * g)))
-    edg = np.abs(do) * (np.abs(da) * eu + (np.abs(u) + eu) * dda)
-    edg = edg + BF * (np.abs(ref["dg"]) + edg)
-    edu = np.abs(do) * ((np.abs(da) + 1.2 * eg) * eg + ez * np.abs(a))
-    edu = edu + BF * (np.abs(ref["du"]) + edu)
-    ag, au = np.abs(ref["dg"]) + edg, np.abs(ref["du"]) + edu
-    tol = {
-        "dx": edg @ np.abs(wg) + edu @ np.abs(wu) + (2 * F / 16 + 12) * ULP * (ag @ np.abs(wg) + au @ np.abs(wu)),
-        "dw_gate": edg.T @ np.abs(x) + (N / 16 + 6) * ULP * (ag.T @ np.abs(x)),
-        "dw_up": edu.T @ np.abs(x) + (N / 16 + 6) * ULP * (au.T @ np.abs(x)),
-    }
-    for k in keys:
-        out = _np(got[k])
-        err = np.abs(out - ref[k])
-        t = BF * np.abs(ref[k]) + 1.01 * tol[k] + 2.0 ** -126
-        assert np.all(err <= t), "%s: worst error / tolerance %.3f" % (k, np.max(err / t))
-        if ref[k].size >= 4096:   # independent roundings: rms 2^-8 / sqrt 3 each, two of them
-            assert np.linalg.norm(out - ref[k]) <= 1.3 * BF * np.sqrt(2 / 3) * np.linalg.norm(ref[k]), k
 
 
 @pytest.mark.parametrize("act", ["silu", "gelu"])
@@ -120,7 +59,7 @@ def test_backward(N, d, F, act, cuda_device):
     (x, wg, wu), do = _inputs(torch, cuda_device, N, d, F, N + d + F)
     got = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act)
     moga.device_status()
-    _check_bwd(got, _np(x), _np(wg), _np(wu), _np(do), act)
+    check_ffn_backward(got, _np(x), _np(wg), _np(wu), _np(do), act)
     again = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act)
     only_x = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act, need_dw=False)
     only_w = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act, need_dx=False)
@@ -143,7 +82,7 @@ def test_large_gates_and_zeros(cuda_device):
             wu[5] = 0
             out = moga.moga_gated_ffn(x, wg, wu, act=act)
             assert torch.isfinite(out.float()).all() and not out[1].any() and not out[:, 5].any()
-            _check_fwd(_np(out), _np(x), _np(wg), _np(wu), act)
+            check_ffn(_np(out), _np(x), _np(wg), _np(wu), act)
             got = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act)
             assert all(torch.isfinite(t.float()).all() for t in got.values())
 
@@ -177,4 +116,4 @@ def test_offsets_past_32_bits(cuda_device):
     got = moga.moga_gated_ffn_backward(big, wg, wu, out, need_dw=False)
     moga.device_status()
     for rows in (slice(N - n, N), slice(0, n)):
-        _check_bwd(dict(dx=got["dx"][rows]), _np(x[:n]), _np(wg), _np(wu), _np(small[:n]), "silu", keys=("dx",))
+        check_ffn_backward(dict(dx=got["dx"][rows]), _np(x[:n]), _np(wg), _np(wu), _np(small[:n]), "silu", keys=("dx",))

@@ -1,20 +1,14 @@
-"""GPU parity of the RMS norm with the residual's addition and of its backward against the fp64 oracle.
-
-Tolerances count roundings.  The kernels' fp32 chain per value is a sum of up
-to 40 squares per thread, a tree of at most 5 + 16 adds, and about ten further
-operations: under 2^7 roundings of 2^-24 at most, so 2^-17 relative to the sum
-of the terms' magnitudes.  A stored value is off by half a step of its type
-more: 2^-24 (fp32, already inside), 2^-8 (bf16), the e4m3 grid's half step.
-"""
+"""GPU parity of the RMS norm with the residual's addition and of its backward against the fp64 oracle
+(tolerances: _block.py)."""
 import numpy as np
 import pytest
 
+from _block import CHAIN, check_norm_backward, check_norm_y
+from _block import to_np as _np
 from oracle import block
 
 pytestmark = pytest.mark.gpu
 
-CHAIN = 2.0 ** -17
-HALF = {"bf16": 2.0 ** -8, "f32": 2.0 ** -24}
 EPS = 1e-6
 
 
@@ -27,10 +21,6 @@ def _rand(torch, dev, shape, dt, seed, scale=1.0):
     return (torch.randn(shape, generator=g, device=dev) * scale).to(_t(torch)[dt])
 
 
-def _np(t):
-    return t.double().cpu().numpy()
-
-
 # one width per thread layout and its borders, the widest, and the least; N of one row, of one CTA's rows and a
 # rest, and above the SM count (where the layout for few rows ends)
 SHAPES = [(1, 8), (5, 64), (149, 136), (3, 768), (300, 776), (1, 1536), (301, 1544), (3, 2560), (150, 2568), (1, 5120),
@@ -39,17 +29,6 @@ TYPES = [("bf16", None, "bf16"), ("bf16", None, "e4m3"), ("f32", None, "f32"), (
          ("f32", None, "e4m3"), ("bf16", "bf16", "bf16"), ("bf16", "bf16", "e4m3"), ("bf16", "f32", "bf16"),
          ("bf16", "f32", "f32"), ("bf16", "f32", "e4m3"), ("f32", "f32", "f32"), ("f32", "f32", "bf16"),
          ("f32", "f32", "e4m3")]
-
-
-def _check_y(y, scale, want, out):
-    if out == "e4m3":
-        s = block.row_scale(want)
-        assert np.all(np.abs(scale - s) <= CHAIN * s)
-        v = want / s[:, None]
-        assert np.all(np.abs(y - v) <= block.e4m3_half_step(v) + CHAIN * np.abs(v))
-        assert np.all(np.max(np.abs(y), axis=1) == 448.0)
-    else:
-        assert np.all(np.abs(y - want) <= (HALF[out] + CHAIN) * np.abs(want))
 
 
 @pytest.mark.parametrize("x_dt,r_dt,out", TYPES)
@@ -68,7 +47,7 @@ def test_forward_matches_oracle(x_dt, r_dt, out, cuda_device):
         else:
             assert torch.equal(h, (x.float() + res.float()).to(res.dtype))   # the stored sum, bit for bit
         want = block.rms_norm(_np(h), _np(w), EPS)[0]
-        _check_y(_np(y.float()), None if scale is None else _np(scale), want, out)
+        check_norm_y(_np(y.float()), None if scale is None else _np(scale), want, out)
 
 
 @pytest.mark.parametrize("dy_dt,h_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
@@ -84,20 +63,12 @@ def test_backward_matches_oracle(dy_dt, h_dt, with_dres, cuda_device):
         branch = torch.bfloat16 if h_dt == "f32" else None
         dx, dw, dxb = moga.moga_rms_norm_backward(dy, h, w, dres=dres, eps=EPS, branch_dtype=branch)
         moga.device_status()
-        h6, dy6, w6 = _np(h), _np(dy), _np(w)
-        rdx, rdw = block.rms_norm_backward(dy6, h6, w6, None if dres is None else _np(dres), EPS)
-        _, r = block.rms_norm(h6, w6, EPS)
-        terms = r * (np.abs(dy6 * w6) + np.abs(h6) * r * r * np.mean(np.abs(dy6 * w6 * h6), axis=1, keepdims=True))
-        if dres is not None:
-            terms = terms + np.abs(_np(dres))
-        assert np.all(np.abs(_np(dx) - rdx) <= HALF[h_dt] * np.abs(rdx) + CHAIN * terms)
+        assert dw.dtype == torch.float32
+        check_norm_backward(_np(dx), _np(dw), _np(dy), _np(h), _np(w), None if dres is None else _np(dres), EPS, h_dt)
         if branch is None:
             assert dxb is None
         else:
             assert torch.equal(dxb, dx.to(torch.bfloat16))
-        # dw: at most N sequential adds and the rows' own chains
-        assert dw.dtype == torch.float32
-        assert np.all(np.abs(_np(dw) - rdw) <= (CHAIN + N * 2.0 ** -24) * np.sum(np.abs(dy6 * h6 * r), axis=0))
         # the same again bit for bit; without dw; into dres's own buffer
         dx2, dw2, _ = moga.moga_rms_norm_backward(dy, h, w, dres=dres, eps=EPS)
         assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
@@ -142,7 +113,7 @@ def test_extreme_rows(cuda_device):
     assert torch.isnan(s[4]) and torch.isnan(s[5])
     for r in (1, 6):                # all zero, scale at its floor
         assert float(s[r]) == np.float32(2.0 ** -100) / np.float32(448) and not q[r].float().any()
-    _check_y(_np(q.float())[[0, 3, 7, 8]], _np(s)[[0, 3, 7, 8]], want[[0, 3, 7, 8]], "e4m3")
+    check_norm_y(_np(q.float())[[0, 3, 7, 8]], _np(s)[[0, 3, 7, 8]], want[[0, 3, 7, 8]], "e4m3")
     # row 2: values of 1e-38 (some subnormal) times 1e3; every value within the grid's half step
     v = _np(q.float())[2] * float(s[2])
     assert np.all(np.abs(v - want[2]) <= block.e4m3_half_step(want[2] / float(s[2])) * float(s[2]) * 1.01 + 1e-41)
