@@ -485,6 +485,11 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
           }
         }
       }
+      // A wait that ran out: the copies that nothing will wait for (both CTAs'
+      // arrive on the leader's barriers) land before the CTAs leave.
+      if (!ok && leader)
+        for (int i = c > T::kStages ? c - T::kStages : 0; i < c; ++i)
+          mbar_drain(bar(T::kFull + i % T::kStages), (i / T::kStages) & 1, p.timeout);
     }
     __syncwarp();
   } else if (warp == EW + 1) {

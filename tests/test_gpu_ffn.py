@@ -7,7 +7,7 @@ from _block import to_np as _np
 
 pytestmark = pytest.mark.gpu
 
-SHAPES = [(1, 16, 8), (1, 64, 128), (1, 1536, 264), (2, 80, 136), (7, 528, 96), (8, 128, 16), (9, 256, 520),
+SHAPES = [(1, 16, 8), (100, 16, 8), (2000, 16, 8), (1, 64, 128), (1, 1536, 264), (2, 80, 136), (7, 528, 96), (8, 128, 16), (9, 256, 520),
           (16, 1536, 512), (17, 144, 360), (31, 2048, 128), (32, 96, 1032), (33, 512, 256), (64, 1536, 384),
           (65, 208, 72), (127, 128, 128), (129, 512, 264), (256, 1536, 512), (257, 1552, 1032), (600, 1536, 4096),
           (2100, 64, 2056)]
@@ -67,6 +67,17 @@ def test_backward(N, d, F, act, cuda_device):
         assert torch.equal(got[k], again[k])
     assert only_x["dw_gate"] is None and only_x["dw_up"] is None and torch.equal(only_x["dx"], got["dx"])
     assert only_w["dx"] is None and torch.equal(only_w["dw_up"], got["dw_up"])
+    moga.device_status()
+
+
+def test_narrowest_bf16(cuda_device):
+    """d = 8: one 16-byte row of x, less than a box on every side."""
+    import torch
+    import sparse_attention_long_moga_b200 as moga
+    for N in (3, 70, 600):
+        (x, wg, wu), do = _inputs(torch, cuda_device, N, 8, 8, N)
+        check_ffn(_np(moga.moga_gated_ffn(x, wg, wu)), _np(x), _np(wg), _np(wu), "silu")
+        check_ffn_backward(moga.moga_gated_ffn_backward(x, wg, wu, do), _np(x), _np(wg), _np(wu), _np(do), "silu")
     moga.device_status()
 
 
