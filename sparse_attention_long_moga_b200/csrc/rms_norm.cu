@@ -409,8 +409,18 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restri
   __shared__ float s[32][33];
   const int c = blockIdx.x * 32 + threadIdx.x, j = threadIdx.y;
   float a = 0.f;
-  if (c < d)
-    for (int r = j; r < rows; r += 32) a += partial[(size_t)r * d + c];
+  if (c < d) {
+    const float* q = partial + c;
+    int r = j;
+    for (; r + 7 * 32 < rows; r += 8 * 32) {   // eight loads under way (up to 23 rows a slice)
+      float v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = q[(size_t)(r + 32 * i) * d];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a += v[i];
+    }
+    for (; r < rows; r += 32) a += q[(size_t)r * d];
+  }
   s[j][threadIdx.x] = a;
   __syncthreads();
   if (j == 0 && c < d) {
