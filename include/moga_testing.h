@@ -55,9 +55,9 @@
  * on `sms` SMs: with grad = 0 its tiles of bn accumulator columns, with
  * grad = 1 the units of the gradient launch (dx tiles where need_dx, dW units
  * where need_dw).  For unit i < min(n, cap), pair by pair in the order that
- * the pair takes them, out[8i .. 8i+7] = (pair, kind (0 gated tile, 1 dx tile,
+ * the pair takes them, out[10i .. 10i+9] = (pair, kind (0 gated tile, 1 dx tile,
  * 2 dW unit), up matrix, row tile, column tile, split, first k stage, end k
- * stage).  Host code only.
+ * stage, first 256-row half of the tile, end half).  Host code only.
  */
 #ifndef MOGA_TESTING_H
 #define MOGA_TESTING_H

@@ -82,7 +82,8 @@ struct Params {
   int mf_tiles;              // row tiles of F
   Kind kind[2];              // dx, dW
   int first;                 // the kind whose units each pair takes first
-  int n1, a, b;              // units of the other kind for the first n1 pairs, for the others
+  int hm;                    // 256-row halves of a tile (the kernel's HM)
+  int n1, a, b;              // halves of units of the other kind for the first n1 pairs, for the others
   long long timeout;
 };
 
@@ -90,6 +91,7 @@ struct Params {
 struct Unit {
   int kind;                  // 0: gated tile, 1: dx tile, 2: dW tile
   int m, n, k0, k1, split, up;
+  int h0, h1;                // its halves (GRAD: [0, hm), or one of them)
 };
 
 // Tile t -> (row tile, column tile).  Tiles run down bands of kGroupM row
@@ -109,12 +111,15 @@ __host__ __device__ __forceinline__ void tile_of(int t, int m_tiles, int n_tiles
 // split where a tile would take longer than a pair's share of all the work
 // (grad_shape), and the longer units go first: unit j P + pair of the first
 // kind for each pair, then units of the other kind, of which the n1 pairs that
-// hold one more of the first take `a` and the others `b`, the difference being
-// about the length of one (plan_grad).
+// hold one more of the first take fewer, about the length of one (plan_grad).
+// 512-row tiles of the other kind are counted in halves, and a pair with an odd
+// number ends on a single half: 32,760 x 1536 x 4096 takes 10.5 rounds of dx
+// tiles instead of 11.
 // The j-th unit of pair `pair` of `P`; false when it has no more.
 template <int MODE>
 __host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int P, int j, Unit* u) {
-  u->split = u->up = 0;
+  u->split = u->up = u->h0 = 0;
+  u->h1 = MODE == MODE_GRAD ? p.hm : 1;
   if (MODE != MODE_GRAD) {
     const int t = j * P + pair;   // total < 2^30, P < 2^10: no overflow where the loop stops at the first false
     if (t >= p.total) return false;
@@ -129,9 +134,19 @@ __host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int 
   int which = p.first, t = j * P + pair;
   if (j >= mine) {
     which ^= 1;
-    const int i = j - mine;
-    if (i >= (pair < p.n1 ? p.a : p.b)) return false;
-    t = i < p.a || p.n1 == 0 ? i * P + pair : p.a * P + (i - p.a) * (P - p.n1) + pair - p.n1;
+    const int i = j - mine, halves = pair < p.n1 ? p.a : p.b;
+    const int fa = p.a / p.hm, fb = p.b / p.hm;      // whole units of either group of pairs
+    if (i < halves / p.hm) {
+      t = i < fa || p.n1 == 0 ? i * P + pair : fa * P + (i - fa) * (P - p.n1) + pair - p.n1;
+    } else {
+      if (i > halves / p.hm || halves % p.hm == 0) return false;
+      // the pair's last: one half, of the tiles that no pair takes whole
+      const int rank = pair < p.n1 || p.a % 2 == 1 ? pair : pair - p.n1;
+      const int h = 2 * (p.n1 * fa + (P - p.n1) * fb) + rank;
+      t = h >> 1;
+      u->h0 = h & 1;
+      u->h1 = u->h0 + 1;
+    }
     if (t >= p.kind[which].units) return false;
   }
   const Kind& kd = p.kind[which];
@@ -457,7 +472,8 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
           const bool peer_a = MODE == MODE_GRAD || (u.m * 2 + 1) * BM < p.rows;
           // the leader's barrier expects both CTAs' bytes
           if (leader) {
-            const int a_bytes = MODE == MODE_GRAD ? 2 * T::kABytes : (peer_a ? 2 : 1) * p.a_box * kRowBytes;
+            const int a_bytes = MODE == MODE_GRAD ? 2 * (u.h1 - u.h0) * BM * kRowBytes
+                                                  : (peer_a ? 2 : 1) * p.a_box * kRowBytes;
             mbar_arrive_expect_tx(bar(T::kFull + st), a_bytes + 2 * T::kBBytes);
           }
           const uint32_t a = sbase + st * T::kStageBytes, b = a + T::kABytes;
@@ -471,14 +487,13 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
               const bool up = kt >= p.seg_k;
               const int k0 = (up ? kt - p.seg_k : kt) * BK;
               const CUtensorMap *ma = up ? &maps.m[4] : &maps.m[3], *mb = up ? &maps.m[2] : &maps.m[1];
-#pragma unroll
-              for (int i = 0; i < 2 * HM; ++i) tma_load_2d_pair(a + i * kHalfBox, ma, k0, r0 + 64 * i, full);
+              for (int i = 2 * u.h0; i < 2 * u.h1; ++i) tma_load_2d_pair(a + i * kHalfBox, ma, k0, r0 + 64 * i, full);
               tma_load_2d_pair(b, mb, c0, k0, full);
               tma_load_2d_pair(b + kHalfBox, mb, c0 + 64, k0, full);
             } else {
               const CUtensorMap* ma = u.up ? &maps.m[4] : &maps.m[3];
-#pragma unroll
-              for (int i = 0; i < 2 * HM; ++i) tma_load_2d_pair(a + i * kHalfBox, ma, r0 + 64 * i, kt * BK, full);
+              for (int i = 2 * u.h0; i < 2 * u.h1; ++i)
+                tma_load_2d_pair(a + i * kHalfBox, ma, r0 + 64 * i, kt * BK, full);
               tma_load_2d_pair(b, &maps.m[0], c0, kt * BK, full);
               tma_load_2d_pair(b + kHalfBox, &maps.m[0], c0 + 64, kt * BK, full);
             }
@@ -511,6 +526,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
           const uint32_t sb = sbase + st * T::kStageBytes + T::kABytes;
 #pragma unroll
           for (int h = 0; h < HM; ++h) {
+            if (HM == 2 && (h < u.h0 || h >= u.h1)) continue;
             if (h == 1 && kt == u.k0) {
               if (!(ok = mbar_wait(bar(T::kAccEmpty + 1), empty_parity, abort_flag, p.timeout))) break;
               tc_fence_after();
@@ -566,6 +582,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
       tc_fence_after();
 #pragma unroll 1
       for (int h = 0; h < HM; ++h) {
+        if (HM == 2 && (h < u.h0 || h >= u.h1)) continue;   // a single half is its pair's last unit
         const uint32_t acc = tmem + lane_addr + (HM == 1 ? b : h) * BN;
         const uint32_t empty = peer_addr(bar(T::kAccEmpty + (HM == 1 ? b : h)), 0);
         if constexpr (MODE == MODE_FWD)
@@ -914,16 +931,18 @@ inline int plan_grad(Params& p, const GradShape& g, int64_t N, int d, int F, boo
   const Kind &one = p.kind[p.first], &two = p.kind[p.first ^ 1];
   const int P = (int)std::min<int64_t>((int64_t)one.units + two.units, pair_count(sms));
   p.n1 = one.units % P;
-  const int lag = ceil_div(one.unit_k, two.unit_k);   // units of the second kind in the time of one of the first
-  auto holds = [&](int b) { return (int64_t)p.n1 * std::max(0, b - lag) + (int64_t)(P - p.n1) * b >= two.units; };
-  int lo = 0, hi = two.units;
+  p.hm = g.hm;
+  const int lag = ceil_div(g.hm * one.unit_k, two.unit_k);   // halves of the second kind in the time of one of the first
+  const int64_t all = (int64_t)g.hm * two.units;
+  auto holds = [&](int64_t b) { return p.n1 * std::max<int64_t>(0, b - lag) + (P - p.n1) * b >= all; };
+  int64_t lo = 0, hi = all;
   while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
+    const int64_t mid = lo + (hi - lo) / 2;
     if (holds(mid)) hi = mid;
     else lo = mid + 1;
   }
-  p.b = lo;
-  p.a = p.n1 ? std::max(0, lo - lag) : lo;
+  p.b = (int)lo;
+  p.a = p.n1 ? std::max(0, p.b - lag) : p.b;
   return P;
 }
 
@@ -1068,8 +1087,8 @@ extern "C" int64_t moga_test_ffn_units(int32_t grad, int64_t N, int32_t d, int32
   for (int pair = 0; pair < P; ++pair)
     for (int j = 0; grad ? unit_of<MODE_GRAD>(p, pair, P, j, &u) : unit_of<MODE_FWD>(p, pair, P, j, &u); ++j, ++n)
       if (n < cap) {
-        const int32_t v[8] = {pair, u.kind, u.up, u.m, u.n, u.split, u.k0, u.k1};
-        for (int i = 0; i < 8; ++i) out[8 * n + i] = v[i];
+        const int32_t v[10] = {pair, u.kind, u.up, u.m, u.n, u.split, u.k0, u.k1, u.h0, u.h1};
+        for (int i = 0; i < 10; ++i) out[10 * n + i] = v[i];
       }
   return n;
 }

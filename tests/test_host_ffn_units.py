@@ -21,7 +21,7 @@ def units():
 
     def call(*a):
         n = fn(*a, None, 0)
-        out = np.zeros((n, 8), dtype=np.int32)
+        out = np.zeros((n, 10), dtype=np.int32)
         assert fn(*a, out.ctypes.data_as(ctypes.c_void_p), n) == n
         return out
     return call
@@ -54,13 +54,16 @@ def test_gradient_units(units, sms):
             # rows of a tile: 512, or 256 where there would be few tiles
             rows = 512 if 2 * nt * (ceil(N, 512) + 2 * ceil(F, 512)) >= 3 * max(1, sms // 2) else 256
             assert not dx[:, 2].any()
-            x_tiles = {(0, m, n) for m in range(ceil(N, rows)) for n in range(nt)} if need_dx else set()
-            tiles = {(up, m, n) for up in (0, 1) for m in range(ceil(F, rows)) for n in range(nt)} if need_dw else set()
+            halves = range(rows // 256)
+            x_tiles = {(0, m, n, h) for m in range(ceil(N, rows)) for n in range(nt) for h in halves}
+            tiles = {(up, m, n, h) for up in (0, 1) for m in range(ceil(F, rows)) for n in range(nt) for h in halves}
+            x_tiles, tiles = x_tiles if need_dx else set(), tiles if need_dw else set()
             for part, want, stages in ((dx, x_tiles, 2 * ceil(F, 64)), (dw, tiles, ceil(N, 64))):
                 seen = {}
-                for _, _, up, m, n, split, k0, k1 in part.tolist():
-                    assert 0 <= k0 < k1 <= stages
-                    seen.setdefault((up, m, n), []).append((split, k0, k1))
+                for _, _, up, m, n, split, k0, k1, h0, h1 in part.tolist():
+                    assert 0 <= k0 < k1 <= stages and 0 <= h0 < h1 <= rows // 256
+                    for h in range(h0, h1):
+                        seen.setdefault((up, m, n, h), []).append((split, k0, k1))
                 assert set(seen) == want
                 for parts in seen.values():
                     parts.sort()
@@ -69,10 +72,12 @@ def test_gradient_units(units, sms):
                     assert all(a[2] == b[1] for a, b in zip(parts, parts[1:]))
             # no pair is given much more than its share: within two of the longest units of the mean
             if len(u):
-                cost = np.bincount(u[:, 0], weights=u[:, 7] - u[:, 6])
-                longest = (u[:, 7] - u[:, 6]).max()
+                work = (u[:, 7] - u[:, 6]) * (u[:, 9] - u[:, 8])
                 pairs = min(len(u), max(1, sms // 2))
-                assert cost.max() <= (u[:, 7] - u[:, 6]).sum() / pairs + 2 * longest
+                assert np.bincount(u[:, 0], weights=work).max() <= work.sum() / pairs + 2 * work.max()
+                # a single half comes last, so that its pair's barriers stay in step
+                single = np.flatnonzero(u[:, 9] - u[:, 8] < rows // 256)
+                assert np.all((single == len(u) - 1) | (u[np.minimum(single + 1, len(u) - 1), 0] != u[single, 0]))
 
 
 @pytest.mark.parametrize("bn", [128, 256])
