@@ -249,7 +249,13 @@ rms_norm_kernel(const FwdParams p) {
   const float top = amax < kScaleFloor ? kScaleFloor : amax;
   // the short way where neither 448 / max|h w| nor the floor matters
   const bool direct = amax >= kScaleFloor && mx >= kScaleFloor;
-  const float k1 = direct ? 1.f : rstd, k2 = kE4m3Max / (direct ? mx : top);
+  const float k2 = kE4m3Max / (direct ? mx : top);
+  if (!direct) {   // t 448 / max|h w| = (t r) 448 / top
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[i][j] *= rstd;
+  }
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     const int v = li + i * TPR;
@@ -258,7 +264,7 @@ rms_norm_kernel(const FwdParams p) {
       float q[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        q[j] = (f[i][j] * k1) * k2;
+        q[j] = f[i][j] * k2;
         // within 8 units of a tie of the 3-bit mantissa; the four roundings above are worth 4 at most
         near |= (__float_as_uint(q[j]) << 12) - ((0x80000u - 8u) << 12) <= 16u << 12;
       }
