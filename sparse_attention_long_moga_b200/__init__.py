@@ -50,7 +50,7 @@ def _need(t, dtype, name, dim=None, shape=None, device=True):
         raise ValueError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if dim is not None and t.dim() != dim:
         raise ValueError("%s must have %d dims" % (name, dim))
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
     if not t.is_contiguous():
         raise ValueError("%s must be contiguous" % name)
@@ -505,6 +505,12 @@ _NORM_DT = {torch.float32: MOGA_F32, torch.bfloat16: MOGA_BF16, torch.float8_e4m
 _ACTS = {"silu": MOGA_ACT_SILU, "gelu": MOGA_ACT_GELU}
 
 
+def _addr(t):
+    # a plain int, which the declared argument types turn into a pointer: these calls are often as short as their
+    # marshalling
+    return t.data_ptr() if t is not None else None
+
+
 def _float_dt(t, name):
     if t.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
@@ -538,8 +544,8 @@ def moga_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor 
         h = torch.empty_like(residual)
     y = torch.empty_like(x, dtype=out_dtype)
     scale = x.new_empty(N, dtype=torch.float32) if out_dtype == torch.float8_e4m3fn else None
-    check(lib().moga_rms_norm(_ptr(x), x_dt, _ptr(residual), r_dt, _ptr(weight), w_dt, N, d, eps, _ptr(h), _ptr(y),
-                              _NORM_DT[out_dtype], _ptr(scale), _stream()), "moga_rms_norm")
+    check(lib().moga_rms_norm(_addr(x), x_dt, _addr(residual), r_dt, _addr(weight), w_dt, N, d, eps, _addr(h), _addr(y),
+                              _NORM_DT[out_dtype], _addr(scale), _stream()), "moga_rms_norm")
     return y, x if residual is None else h, scale
 
 
@@ -571,8 +577,8 @@ def moga_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tens
     if need_dw:
         dw = h.new_empty(d, dtype=torch.float32)
         ws = h.new_empty(max(L.moga_rms_norm_bwd_ws_bytes(N, d), 16), dtype=torch.uint8)
-    check(L.moga_rms_norm_bwd(_ptr(dy), dy_dt, _ptr(h), h_dt, _ptr(weight), w_dt, _ptr(dres), N, d, eps, _ptr(dx),
-                              _ptr(dxb), _ptr(dw), _ptr(ws), ws.numel() if need_dw else 0, _stream()),
+    check(L.moga_rms_norm_bwd(_addr(dy), dy_dt, _addr(h), h_dt, _addr(weight), w_dt, _addr(dres), N, d, eps, _addr(dx),
+                              _addr(dxb), _addr(dw), _addr(ws), ws.numel() if need_dw else 0, _stream()),
           "moga_rms_norm_bwd")
     return dx, dw, dxb
 
@@ -611,8 +617,8 @@ def moga_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ac
             _need(t, torch.float32, name, 1, (n,), device=False)
     _on_device(x=x, w_gate=w_gate, w_up=w_up, x_scale=x_scale, w_gate_scale=w_gate_scale, w_up_scale=w_up_scale)
     out = x.new_empty((N, F), dtype=torch.bfloat16)
-    check(lib().moga_gated_ffn(_ptr(x), _ptr(w_gate), _ptr(w_up), _NORM_DT[x.dtype], _ptr(x_scale),
-                               _ptr(w_gate_scale), _ptr(w_up_scale), N, d, F, _ACTS[act], _ptr(out), _stream()),
+    check(lib().moga_gated_ffn(_addr(x), _addr(w_gate), _addr(w_up), _NORM_DT[x.dtype], _addr(x_scale),
+                               _addr(w_gate_scale), _addr(w_up_scale), N, d, F, _ACTS[act], _addr(out), _stream()),
           "moga_gated_ffn")
     return out
 
@@ -629,6 +635,6 @@ def moga_gated_ffn_backward(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.T
     dx = torch.empty_like(x) if need_dx else None
     dwg, dwu = (torch.empty_like(w_gate) if need_dw else None for _ in range(2))
     ws = x.new_empty(max(L.moga_gated_ffn_bwd_ws_bytes(N, d, F), 16), dtype=torch.uint8)
-    check(L.moga_gated_ffn_bwd(_ptr(x), _ptr(w_gate), _ptr(w_up), N, d, F, _ACTS[act], _ptr(dout), _ptr(dx),
-                               _ptr(dwg), _ptr(dwu), _ptr(ws), ws.numel(), _stream()), "moga_gated_ffn_bwd")
+    check(L.moga_gated_ffn_bwd(_addr(x), _addr(w_gate), _addr(w_up), N, d, F, _ACTS[act], _addr(dout), _addr(dx),
+                               _addr(dwg), _addr(dwu), _addr(ws), ws.numel(), _stream()), "moga_gated_ffn_bwd")
     return dict(dx=dx, dw_gate=dwg, dw_up=dwu)
