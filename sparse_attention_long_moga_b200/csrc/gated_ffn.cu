@@ -172,6 +172,12 @@ __device__ __forceinline__ void mma_pair_f8(uint32_t d_tmem, uint64_t adesc, uin
       : "memory");
 }
 
+// The backward's launches follow one another with programmatic dependent
+// launch: the next one's CTAs are set up while the last of this one's finish,
+// and wait for its memory where they first read it.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Activation and its derivative in fp32.  silu: g s, s = 1 / (1 + e^-g);
 // gelu: the tanh form, 0.5 (1 + tanh z) = 1 / (1 + e^-2z),
 // z = sqrt(2 / pi) (g + 0.044715 g^3).  e^-x overflows to infinity for large
@@ -429,6 +435,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
   const uint32_t rank = cluster_rank();          // 0: leader, 1: peer
   const bool leader = rank == 0;
   const int pair = blockIdx.x >> 1, n_pairs = gridDim.x >> 1;
+  if (MODE != MODE_FWD) let_next_start();
 
   if (threadIdx.x == 0) {
     *abort_flag = 0;
@@ -458,6 +465,7 @@ ffn_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) 
   if (warp == EW) {
     // ------------------------------------------------------------------ producer
     if (lane == 0) {
+      if (MODE == MODE_GRAD) wait_for_previous();   // dg and du
       int c = 0;
       bool ok = true;
       Unit u;
@@ -620,6 +628,7 @@ struct SumParams {
   uint4 *dx, *dwg, *dwu;
 };
 __global__ void __launch_bounds__(256) ffn_sum_kernel(const SumParams p) {
+  wait_for_previous();
   int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const bool w = i >= p.nx;
   if (w) i -= p.nx;
@@ -789,12 +798,33 @@ static moga_status make_map(CUtensorMap* m, const void* base, int64_t rows, int6
   return MOGA_OK;
 }
 
+// a launch that may be set up before the one in front of it on the stream ends
+template <class... Params_, class... Args>
+static moga_status launch_next(void (*k)(Params_...), unsigned grid, int threads, int smem, cudaStream_t s,
+                               const char* who, const Args&... args) {
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+  if (e != cudaSuccess) return fail(MOGA_ERR_CUDA, "%s: %s", who, cudaGetErrorString(e));
+  return check_launch(who);
+}
+
 template <int MODE, bool E4M3, int ACT, int BN, int HM, int EW>
 static moga_status launch(const Params& p, const Maps& maps, int pairs, const char* who, cudaStream_t s) {
   auto* k = ffn_kernel<MODE, E4M3, ACT, BN, HM, EW>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<BN, HM, boxes_of(MODE, EW)>::kSmemBytes);
   if (e != cudaSuccess) return fail(MOGA_ERR_CUDA, "%s: cudaFuncSetAttribute: %s", who, cudaGetErrorString(e));
-  k<<<2 * pairs, (EW + 2) * 32, Tile<BN, HM, boxes_of(MODE, EW)>::kSmemBytes, s>>>(p, maps);
+  constexpr int smem = Tile<BN, HM, boxes_of(MODE, EW)>::kSmemBytes;
+  if (MODE == MODE_GRAD) return launch_next(k, 2 * pairs, (EW + 2) * 32, smem, s, who, p, maps);
+  k<<<2 * pairs, (EW + 2) * 32, smem, s>>>(p, maps);
   return check_launch(who);
 }
 
@@ -1062,8 +1092,7 @@ extern "C" moga_status moga_gated_ffn_bwd(const void* x, const void* w_gate, con
   q.dx = static_cast<uint4*>(dx);
   q.dwg = static_cast<uint4*>(dw_gate);
   q.dwu = static_cast<uint4*>(dw_up);
-  ffn_sum_kernel<<<(unsigned)ceil64(q.nx + 2 * q.nw, 256), 256, 0, s>>>(q);
-  return check_launch(who);
+  return launch_next(ffn_sum_kernel, (unsigned)ceil64(q.nx + 2 * q.nw, 256), 256, 0, s, who, q);
 }
 
 // test hook (moga_testing.h): the units of every pair of one launch
