@@ -13,7 +13,9 @@ kernels do every step of the layer:
     # out = stga_attn_mean(q, k, v, geom, o_acc=o)
     loss = moga_balance_loss(counts, ws, N, M, a)   # L_gb (fp64 scalar)
 
-`visual_attention_forward` chains the six calls.
+`visual_attention_forward` chains the six calls.  For the rest of the block:
+`moga_rms_norm` (with the residual's addition) and `moga_gated_ffn`, each with
+its backward.
 """
 from __future__ import annotations
 
