@@ -436,8 +436,10 @@ moga_status moga_balance_loss_part(const int32_t* counts, const void* route_ws, 
  *   y = h / sqrt(mean(h^2) + eps) * w          (fp32, rounded once)
  * y is taken from the stored h.  An e4m3 output has one scale per row:
  *   scale = max(max|y|, 2^-100) / 448,   y_q = e4m3(y / scale)
- * and stands for y_q * scale.  A row with a NaN or an infinity in h gives NaN
- * values (e4m3: the row's scale is NaN).
+ * and stands for y_q * scale.  A NaN in h makes its whole row of y NaN, an
+ * infinity its own value (and the others 0); in e4m3 the scale of such a row is
+ * NaN (where w is not 0).  A row whose sum of squares passes the fp32 range
+ * gives zeros.
  * x:        [N][d], x_dt (MOGA_F32 or MOGA_BF16)
  * residual: [N][d], res_dt, or NULL.  Pairs (x, residual): bf16 + bf16,
  *           bf16 + fp32, fp32 + fp32; fp32 + bf16 is MOGA_ERR_UNSUPPORTED
