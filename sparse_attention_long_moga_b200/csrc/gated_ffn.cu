@@ -47,7 +47,6 @@ constexpr int BM = 128;                      // accumulator rows per CTA (256 pe
 constexpr int kRowBytes = 128;               // bytes of one operand row in a stage (one swizzle span)
 constexpr int kHalfBox = 64 * kRowBytes;     // 8 KB: a box of 64 rows
 constexpr int kOutBox = 32 * kRowBytes;      // 4 KB: a warp's 32 rows x 64 bf16 columns of output
-constexpr int kGroupM = 8;                   // row tiles per band of the tile order
 
 // Shared memory of a CTA: operand stages, then the epilogue's output boxes.
 // Accumulators: HM = 1: 256 rows per pair, two buffers of BN columns;
@@ -78,6 +77,7 @@ struct Params {
   int rows, cols;            // FWD, DGDU: N, F;  GRAD: N, d
   int n_k;                   // k stages of a forward tile
   int m_tiles, n_tiles;      // row tiles of N (256 HM rows), column tiles of F (FWD, DGDU) or d (GRAD)
+  int high;                  // row tiles of a band (tile_of)
   int a_box;                 // FWD, DGDU: rows of a box of x
   int total;                 // FWD, DGDU: tiles
   int act;
@@ -101,15 +101,15 @@ struct Unit {
   int h0, h1;                // its halves (GRAD: [0, hm), or one of them)
 };
 
-// Tile t -> (row tile, column tile).  Tiles run down bands of kGroupM row
-// tiles, so that the pairs at work at one time share a few row tiles and a
-// few column tiles in L2 instead of sweeping all of W for every row tile.
-__host__ __device__ __forceinline__ void tile_of(int t, int m_tiles, int n_tiles, int* m, int* n) {
-  const int band = kGroupM * n_tiles;
+// Tile t -> (row tile, column tile).  Tiles run down bands of `high` row tiles,
+// so that the pairs at work at one time share a few row tiles and a few column
+// tiles in L2 instead of sweeping all of W for every row tile.
+__host__ __device__ __forceinline__ void tile_of(int t, int high, int m_tiles, int n_tiles, int* m, int* n) {
+  const int band = high * n_tiles;
   const int b = t / band, r = t - b * band;
-  const int gm = m_tiles - b * kGroupM < kGroupM ? m_tiles - b * kGroupM : kGroupM;
+  const int gm = m_tiles - b * high < high ? m_tiles - b * high : high;
   *n = r / gm;
-  *m = b * kGroupM + (r - *n * gm);
+  *m = b * high + (r - *n * gm);
 }
 
 // Gradient units.  dW's tiles are 2 F / 256 x d / 256 with K = N, dx's N / 256
@@ -133,7 +133,7 @@ __host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int 
     u->kind = 0;
     u->k0 = 0;
     u->k1 = p.n_k;
-    tile_of(t, p.m_tiles, p.n_tiles, &u->m, &u->n);
+    tile_of(t, p.high, p.m_tiles, p.n_tiles, &u->m, &u->n);
     return true;
   }
   const int n_first = p.kind[p.first].units;
@@ -160,7 +160,7 @@ __host__ __device__ __forceinline__ bool unit_of(const Params& p, int pair, int 
   const int mt = which == 0 ? p.m_tiles : 2 * p.mf_tiles, tiles = mt * p.n_tiles;
   u->kind = 1 + which;
   u->split = t / tiles;
-  tile_of(t - u->split * tiles, mt, p.n_tiles, &u->m, &u->n);
+  tile_of(t - u->split * tiles, p.high, mt, p.n_tiles, &u->m, &u->n);
   if (which == 1 && u->m >= p.mf_tiles) {
     u->up = 1;
     u->m -= p.mf_tiles;
@@ -858,6 +858,13 @@ static moga_status check_dims(const char* who, int64_t N, int32_t d, int32_t F, 
   return MOGA_OK;
 }
 
+// Row tiles of a forward band.  The weights are read once per band: where both
+// do not stay in L2's near half (64 MB), higher bands read them less often
+// (16,380 x 5120 x 13824 in e4m3: 1681 us with 8, 1637 with 16, 1632 with 32;
+// 8190 tokens in bf16: 1539, 1516, 1622), else low ones keep x closer (32,760 x
+// 1536 x 4096: 551, 557, 555).
+inline int band_tiles(int64_t d, int64_t F, int elem) { return 2 * F * d * elem > (64 << 20) ? 16 : 8; }
+
 // The gated product over all tokens with tiles of BN accumulator columns.
 template <int MODE, bool E4M3, int BN>
 static moga_status launch_gated_bn(Params p, const void* x, const void* wg, const void* wu, int d, void* o0, void* o1,
@@ -877,6 +884,7 @@ static moga_status launch_gated_bn(Params p, const void* x, const void* wg, cons
   p.m_tiles = ceil_div(p.rows, 2 * BM);
   p.n_tiles = ceil_div(p.cols, BN / 2);
   p.total = p.m_tiles * p.n_tiles;
+  p.high = band_tiles(d, p.cols, elem);
   const int pairs = std::min(p.total, pair_count(sms));
   // Epilogue warps: eight, one for each 64 columns of the tile's rows.  For dg
   // and du, whose 16 boxes then cost an operand stage, only where the epilogue
@@ -978,6 +986,7 @@ inline int plan_grad(Params& p, const GradShape& g, int64_t N, int d, int F, boo
   const int P = (int)std::min<int64_t>((int64_t)one.units + two.units, pair_count(sms));
   p.n1 = one.units % P;
   p.hm = g.hm;
+  p.high = 8 / g.hm;   // 2048 rows a band (512-row tiles, 32,760 x 1536 x 4096: 1078 us with 4, 1097 with 8)
   const int lag = ceil_div(g.hm * one.unit_k, two.unit_k);   // halves of the second kind in the time of one of the first
   const int64_t all = (int64_t)g.hm * two.units;
   auto holds = [&](int64_t b) { return p.n1 * std::max<int64_t>(0, b - lag) + (P - p.n1) * b >= all; };
@@ -1125,6 +1134,7 @@ extern "C" int64_t moga_test_ffn_units(int32_t grad, int64_t N, int32_t d, int32
     p.m_tiles = (int)ceil64(N, 2 * ffn::BM);
     p.n_tiles = ceil_div(F, bn / 2);
     p.total = p.m_tiles * p.n_tiles;
+    p.high = band_tiles(d, F, 2);
     P = std::min(p.total, pair_count(sms));
   }
   int64_t n = 0;
