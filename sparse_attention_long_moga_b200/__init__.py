@@ -513,10 +513,14 @@ def _addr(t):
     return t.data_ptr() if t is not None else None
 
 
+_FLOAT_DT = {torch.float32: MOGA_F32, torch.bfloat16: MOGA_BF16}
+
+
 def _float_dt(t, name):
-    if t.dtype not in (torch.float32, torch.bfloat16):
+    dt = _FLOAT_DT.get(t.dtype)
+    if dt is None:
         raise ValueError("%s must be float32 or bfloat16, got %s" % (name, t.dtype))
-    return _NORM_DT[t.dtype]
+    return dt
 
 
 def moga_rms_norm(x: torch.Tensor, weight: torch.Tensor, residual: torch.Tensor | None = None, eps: float = 1e-6,
@@ -608,18 +612,21 @@ def moga_gated_ffn(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, ac
     if x.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
         raise ValueError("x must be bfloat16 or float8_e4m3fn, got %s" % x.dtype)
     N, d, F = _check_ffn(x, w_gate, w_up, act)
-    scales = (("x_scale", x_scale, N), ("w_gate_scale", w_gate_scale, F), ("w_up_scale", w_up_scale, F))
-    for name, t, n in scales:
-        if x.dtype == torch.bfloat16:
-            if t is not None:
-                raise ValueError("%s goes with float8_e4m3fn operands" % name)
-        elif t is None:
-            raise ValueError("float8_e4m3fn operands need %s" % name)
-        else:
-            _need(t, torch.float32, name, 1, (n,), device=False)
-    _on_device(x=x, w_gate=w_gate, w_up=w_up, x_scale=x_scale, w_gate_scale=w_gate_scale, w_up_scale=w_up_scale)
+    f8 = x.dtype == torch.float8_e4m3fn
+    if f8 or x_scale is not None or w_gate_scale is not None or w_up_scale is not None:
+        for name, t, n in (("x_scale", x_scale, N), ("w_gate_scale", w_gate_scale, F), ("w_up_scale", w_up_scale, F)):
+            if not f8:
+                if t is not None:
+                    raise ValueError("%s goes with float8_e4m3fn operands" % name)
+            elif t is None:
+                raise ValueError("float8_e4m3fn operands need %s" % name)
+            else:
+                _need(t, torch.float32, name, 1, (n,), device=False)
+        _on_device(x=x, w_gate=w_gate, w_up=w_up, x_scale=x_scale, w_gate_scale=w_gate_scale, w_up_scale=w_up_scale)
+    else:
+        _on_device(x=x, w_gate=w_gate, w_up=w_up)
     out = x.new_empty((N, F), dtype=torch.bfloat16)
-    check(lib().moga_gated_ffn(_addr(x), _addr(w_gate), _addr(w_up), _NORM_DT[x.dtype], _addr(x_scale),
+    check(lib().moga_gated_ffn(_addr(x), _addr(w_gate), _addr(w_up), MOGA_E4M3 if f8 else MOGA_BF16, _addr(x_scale),
                                _addr(w_gate_scale), _addr(w_up_scale), N, d, F, _ACTS[act], _addr(out), _stream()),
           "moga_gated_ffn")
     return out
