@@ -308,9 +308,10 @@ struct BwdParams {
 // that an SM holds many rows in different phases and the loads of some are
 // under way while others are at their sums (bwd_shape).  63,960 x 1536, bf16
 // dy, fp32 h: 233 us, 6.7 TB/s, against 276 us of four rows a CTA with three
-// vectors a thread; bf16 h: 139 us, 5.7 TB/s.
-template <int GROUPS, int VPT, class DT, class HT>
-__global__ void __launch_bounds__(GROUPS > 1 ? 32 * GROUPS : VPT == 1 || (VPT == 2 && sizeof(HT) == 2) ? 1024 : 512)
+// vectors a thread; bf16 h: 129 us, 6.1 TB/s.
+template <int GROUPS, int VPT, class DT, class HT, bool AHEAD = false>
+__global__ void __launch_bounds__(GROUPS > 1 ? 32 * GROUPS
+                                  : !AHEAD && (VPT == 1 || (VPT == 2 && sizeof(HT) == 2)) ? 1024 : 512)
 rms_norm_bwd_kernel(const BwdParams p) {
   extern __shared__ float s_dw[];                 // [d] when there is more than one group
   __shared__ float2 red[2][32];
@@ -322,18 +323,47 @@ rms_norm_bwd_kernel(const BwdParams p) {
   for (int i = 0; i < VPT; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  // AHEAD: the next row's vectors, on their way while this one is worked on
+  typename Vec<DT>::type dn[AHEAD ? VPT : 1];
+  typename Vec<HT>::type hn[AHEAD ? VPT : 1], sn[AHEAD ? VPT : 1];
+  auto load = [&](int row, typename Vec<DT>::type* dt, typename Vec<HT>::type* ht, typename Vec<HT>::type* st) {
+    const size_t base = (size_t)row * p.d;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * tpr;
+      if (v < nv) {
+        dt[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
+        ht[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
+        if (p.dres) st[i] = Vec<HT>::load(static_cast<const HT*>(p.dres) + base + 8 * v);
+      }
+    }
+  };
+  const int step = gridDim.x * GROUPS;
+  if constexpr (AHEAD) {
+    if (blockIdx.x * GROUPS + group < p.N) load(blockIdx.x * GROUPS + group, dn, hn, sn);
+  }
   int par = 0;
   for (int row = blockIdx.x * GROUPS + group; row < p.N; row += gridDim.x * GROUPS, par ^= 1) {
     const size_t base = (size_t)row * p.d;
     typename Vec<DT>::type dv[VPT];
     typename Vec<HT>::type hv[VPT], sv[VPT];
+    if constexpr (AHEAD) {
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = li + i * tpr;
-      if (v < nv) {
-        dv[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
-        hv[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
-        if (p.dres) sv[i] = Vec<HT>::load(static_cast<const HT*>(p.dres) + base + 8 * v);
+      for (int i = 0; i < VPT; ++i) {
+        dv[i] = dn[i];
+        hv[i] = hn[i];
+        sv[i] = sn[i];
+      }
+      if (row + step < p.N) load(row + step, dn, hn, sn);
+    } else {
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = li + i * tpr;
+        if (v < nv) {
+          dv[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
+          hv[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
+          if (p.dres) sv[i] = Vec<HT>::load(static_cast<const HT*>(p.dres) + base + 8 * v);
+        }
       }
     }
     float ss = 0.f, dot = 0.f;
@@ -499,19 +529,25 @@ static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_
 // Bytes on the way decide between one and two vectors: two where a bf16 row's
 // vectors are small or where one would leave an SM's threads unused
 // (32,760 x 5120, fp32 h: 526 us with one vector, 367 with two).
+// A bf16 row's vectors are small: where 512 threads fill up, they keep the next
+// row's under way as well (at 110 registers; 63,960 x 1536: 129 against 138 us
+// with 1024 threads that do not, 20,000 x 8192: 210 against 231; 5120, of whose
+// 320-thread CTAs only one would fit: 266 against 236).
 struct BwdShape {
   int threads, vpt, per_sm;
+  bool ahead;
 };
 constexpr int kWarpRow = 768;
 inline BwdShape bwd_shape(int d, bool h_f32) {
-  if (d <= 256) return {256, 1, 3};
-  if (d <= kWarpRow) return {256, 3, 2};
+  if (d <= 256) return {256, 1, 3, false};
+  if (d <= kWarpRow) return {256, 3, 2, false};
   auto threads = [d](int vpt) { return (ceil_div(d / 8, vpt) + 31) / 32 * 32; };
   const int t1 = threads(1), t2 = threads(2);
-  if (!h_f32) return {t2, 2, std::max(1, 1024 / t2)};
-  if (d > 8192) return {threads(4), 4, std::max(1, 512 / threads(4))};
-  if (1024 / t1 * t1 >= 896) return {t1, 1, 1024 / t1};
-  return {t2, 2, std::max(1, 640 / t2)};
+  if (!h_f32 && t2 <= 512 && 512 / t2 * t2 >= 448) return {t2, 2, 512 / t2, true};
+  if (!h_f32) return {t2, 2, std::max(1, 1024 / t2), false};
+  if (d > 8192) return {threads(4), 4, std::max(1, 512 / threads(4)), false};
+  if (1024 / t1 * t1 >= 896) return {t1, 1, 1024 / t1, false};
+  return {t2, 2, std::max(1, 640 / t2), false};
 }
 inline int bwd_ctas(int64_t N, int d, bool h_f32, int sms) {
   const int rows = d <= kWarpRow ? 8 : 1;
@@ -524,7 +560,8 @@ static moga_status launch_bwd(const BwdParams& p, int ctas, cudaStream_t s) {
   const size_t smem = p.d * sizeof(float);
   if (p.d <= 256) rms_norm_bwd_kernel<8, 1, DT, HT><<<ctas, k.threads, smem, s>>>(p);
   else if (p.d <= kWarpRow) rms_norm_bwd_kernel<8, 3, DT, HT><<<ctas, k.threads, smem, s>>>(p);
-  else if (k.vpt == 2) rms_norm_bwd_kernel<1, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+  else if (k.vpt == 2 && !k.ahead) rms_norm_bwd_kernel<1, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+  else if constexpr (sizeof(HT) == 2) rms_norm_bwd_kernel<1, 2, DT, HT, true><<<ctas, k.threads, 0, s>>>(p);
   else if constexpr (sizeof(HT) == 4) {
     if (k.vpt == 1) rms_norm_bwd_kernel<1, 1, DT, HT><<<ctas, k.threads, 0, s>>>(p);
     else rms_norm_bwd_kernel<1, 4, DT, HT><<<ctas, k.threads, 0, s>>>(p);
