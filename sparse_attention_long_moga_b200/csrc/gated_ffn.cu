@@ -30,7 +30,7 @@
 // Measured (short runs, the same box; in brackets the bare cuBLAS product of
 // the same operands): 32,760 x 1536 x 4096 bf16 forward 513 us, 1608 TFLOP/s
 // (507), dg and du 575 us, gradients 1033 us (474 + 502); e4m3, 16,384 x 5120 x
-// 13824: 1613 us, 2876 TFLOP/s (1464 with one scale for all, 1933 with row
+// 13824: 1589 us, 2919 TFLOP/s (1464 with one scale for all, 1933 with row
 // scales).  Bound by the tensor cores under the power cap and by the operand
 // traffic from L2.
 #include "common.cuh"
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(256) ffn_sum_kernel(const SumParams p) {
 // unrolling measured 47 instead of 43.5 us, half the warps 46; one block per
 // SM as the launch bound lets the loads of a pass stay in registers, 45.8
 // against 50 us).  The warps' sums meet in shared memory in a fixed order.
-// One token through 5120 x 13824: 44.5 us, the weights at 6.4 TB/s.
+// One token through 5120 x 13824: 43.4 us, the weights at 6.5 TB/s.
 
 // Up to 16 tokens this kernel is always the faster (16 tokens, 5120 x 13824:
 // 52 against 64 us; 1536 x 4096: 8.3 against 13.1).  Above, every CTA's read of

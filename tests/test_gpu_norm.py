@@ -106,7 +106,8 @@ def test_extreme_rows(cuda_device):
     w = _rand(torch, cuda_device, (d,), "f32", 6)
     y, _, _ = moga.moga_rms_norm(x, w, out_dtype=torch.float32)
     q, _, s = moga.moga_rms_norm(x, w, out_dtype=f8)
-    want = block.rms_norm(_np(x), _np(w), 1e-6)[0]
+    with np.errstate(invalid="ignore"):   # the rows with NaN and infinity
+        want = block.rms_norm(_np(x), _np(w), 1e-6)[0]
     ok = [0, 1, 3, 7, 8]
     assert np.all(np.abs(_np(y)[ok] - want[ok]) <= CHAIN * np.abs(want[ok]))
     assert torch.isnan(y[4]).all() and torch.isnan(y[5, 9])
