@@ -70,6 +70,20 @@ def test_backward(N, d, F, act, cuda_device):
     moga.device_status()
 
 
+# 512-row gradient tiles: ragged on every side; units that end on a half; K of dx split as well
+@pytest.mark.parametrize("N,d,F,act", [(1100, 1536, 4104, "silu"), (2600, 1288, 3080, "gelu"), (3415, 280, 13232, "silu")])
+def test_backward_of_many_tiles(N, d, F, act, cuda_device):
+    import torch
+    import sparse_attention_long_moga_b200 as moga
+    (x, wg, wu), do = _inputs(torch, cuda_device, N, d, F, N + d + F)
+    got = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act)
+    moga.device_status()
+    check_ffn_backward(got, _np(x), _np(wg), _np(wu), _np(do), act)
+    for kw in (dict(need_dx=False), dict(need_dw=False)):
+        alone = moga.moga_gated_ffn_backward(x, wg, wu, do, act=act, **kw)
+        assert all(torch.equal(got[k], v) for k, v in alone.items() if v is not None)
+
+
 def test_narrowest_bf16(cuda_device):
     """d = 8: one 16-byte row of x, less than a box on every side."""
     import torch

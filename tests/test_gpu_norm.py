@@ -55,7 +55,7 @@ def test_forward_matches_oracle(x_dt, r_dt, out, cuda_device):
 def test_backward_matches_oracle(dy_dt, h_dt, with_dres, cuda_device):
     import torch
     import sparse_attention_long_moga_b200 as moga
-    for i, (N, d) in enumerate(SHAPES + [(2500, 1536), (700, 5120)]):
+    for i, (N, d) in enumerate(SHAPES + [(2500, 1536), (700, 5120), (5000, 136), (3001, 520)]):
         h = _rand(torch, cuda_device, (N, d), h_dt, 10 + i, 3.0)
         dy = _rand(torch, cuda_device, (N, d), dy_dt, 40 + i)
         dres = _rand(torch, cuda_device, (N, d), h_dt, 70 + i) if with_dres else None
