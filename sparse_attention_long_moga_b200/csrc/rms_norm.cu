@@ -97,9 +97,11 @@ __device__ __forceinline__ void load_w(const void* w, bool w_bf16, int col, floa
   }
 }
 
+// sum over WIDTH neighbouring lanes (the whole warp takes part)
+template <int WIDTH = 32>
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = WIDTH / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 // Barrier of the TPR threads of one row (named barrier 1 + group).
@@ -112,8 +114,8 @@ __device__ __forceinline__ void row_sync(int group) {
 // `slots`: TPR / 32 floats of the row's own.
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float* slots, int group, int lane_in_row) {
-  v = warp_sum(v);
-  if (TPR == 32) return v;
+  v = warp_sum<(TPR < 32 ? TPR : 32)>(v);
+  if (TPR <= 32) return v;
   if ((lane_in_row & 31) == 0) slots[lane_in_row >> 5] = v;
   row_sync<TPR>(group);
   float r = slots[0];
@@ -128,14 +130,14 @@ template <int TPR>
 __device__ __forceinline__ void row_max_pair(float& mx, float& me, float* slots, float* slots_e, int group,
                                              int lane_in_row) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
     const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), e2 = __shfl_xor_sync(0xffffffffu, me, o);
     if (m2 > mx || (m2 == mx && e2 > me)) {
       mx = m2;
       me = e2;
     }
   }
-  if (TPR == 32) return;
+  if (TPR <= 32) return;
   if ((lane_in_row & 31) == 0) {
     slots[lane_in_row >> 5] = mx;
     slots_e[lane_in_row >> 5] = me;
@@ -173,48 +175,61 @@ struct FwdParams {
 template <int TPR>
 constexpr int kCtaThreads = TPR > 256 ? TPR : 256;
 
-template <int TPR, int VPT, class XT, class HT, bool RES, class YT>
+// ROWS rows at a time per TPR threads: short rows need several under way per
+// thread to fill the memory's latency.
+template <int TPR, int VPT, int ROWS, class XT, class HT, bool RES, class YT>
 __global__ void __launch_bounds__(kCtaThreads<TPR>)
 rms_norm_kernel(const FwdParams p) {
+  static_assert(TPR <= 32 || ROWS == 1, "rows that share a barrier go one at a time");
   constexpr int kGroups = kCtaThreads<TPR> / TPR;
   constexpr bool kQuant = sizeof(YT) == 1;
-  __shared__ float red[3][kGroups][TPR / 32];
+  __shared__ float red[3][kGroups][TPR > 32 ? TPR / 32 : 1];
   const int group = threadIdx.x / TPR, li = threadIdx.x % TPR;
-  const int row = blockIdx.x * kGroups + group;
-  if (row >= p.N) return;   // whole rows leave together: the row barriers stay complete
+  const int row0 = (blockIdx.x * kGroups + group) * ROWS;
+  // A row's own barrier wants all of its threads, and they leave together; rows
+  // inside a warp stay for its shuffles.
+  if (TPR > 32 && row0 >= p.N) return;
   const int nv = p.d >> 3;
-  const size_t base = (size_t)row * p.d;
-  float f[VPT][8];
-  typename Vec<XT>::type xv[VPT];
-  typename Vec<HT>::type rv[VPT];
+  // vector v of row r
+  auto on = [&](int r, int v) { return v < nv && (TPR > 32 || row0 + r < p.N); };
+  auto at = [&](int r, int v) { return (size_t)(row0 + r) * p.d + 8 * v; };
+  float f[ROWS][VPT][8];
+  typename Vec<XT>::type xv[ROWS][VPT];
+  typename Vec<HT>::type rv[ROWS][VPT];
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = li + i * TPR;
-    if (v < nv) {
-      xv[i] = Vec<XT>::load(static_cast<const XT*>(p.x) + base + 8 * v);
-      if (RES) rv[i] = Vec<HT>::load(static_cast<const HT*>(p.res) + base + 8 * v);
-    }
-  }
-  float ss = 0.f;
+  for (int r = 0; r < ROWS; ++r)
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = li + i * TPR;
-    if (v < nv) {
-      Vec<XT>::widen(xv[i], f[i]);
-      if (RES) {
-        float r[8];
-        Vec<HT>::widen(rv[i], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = Vec<HT>::round(f[i][j] + r[j]);
-        Vec<HT>::store(static_cast<HT*>(p.h) + base + 8 * v, f[i]);
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (on(r, v)) {
+        xv[r][i] = Vec<XT>::load(static_cast<const XT*>(p.x) + at(r, v));
+        if (RES) rv[r][i] = Vec<HT>::load(static_cast<const HT*>(p.res) + at(r, v));
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += f[i][j] * f[i][j];
     }
+  float rstd[ROWS];
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+      const int v = li + i * TPR;
+      if (on(r, v)) {
+        Vec<XT>::widen(xv[r][i], f[r][i]);
+        if (RES) {
+          float t[8];
+          Vec<HT>::widen(rv[r][i], t);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[r][i][j] = Vec<HT>::round(f[r][i][j] + t[j]);
+          Vec<HT>::store(static_cast<HT*>(p.h) + at(r, v), f[r][i]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss += f[r][i][j] * f[r][i][j];
+      }
+    }
+    ss = row_sum<TPR>(ss, red[0][group], group, li);
+    rstd[r] = 1.f / sqrtf(ss / (float)p.d + p.eps);
   }
-  ss = row_sum<TPR>(ss, red[0][group], group, li);
-  const float rstd = 1.f / sqrtf(ss / (float)p.d + p.eps);
-  if (!kQuant) {
+  if constexpr (!kQuant) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = li + i * TPR;
@@ -222,71 +237,78 @@ rms_norm_kernel(const FwdParams p) {
         float w[8];
         load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[i][j] = f[i][j] * rstd * w[j];
-        Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, f[i]);
+        for (int r = 0; r < ROWS; ++r)
+          if (on(r, v)) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[r][i][j] = f[r][i][j] * rstd[r] * w[j];
+            Vec<YT>::store(static_cast<YT*>(p.y) + at(r, v), f[r][i]);
+          }
       }
     }
-    return;
-  }
-  // f becomes t = h w rounded; the largest |t| and its remainder: max|h w| = mx + me
-  float mx = 0.f, me = 0.f;
+  } else {
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = li + i * TPR;
-    if (v < nv) {
-      float w[8];
-      load_w(p.w, p.w_bf16, 8 * v, w);
+    for (int r = 0; r < ROWS; ++r) {
+      // f becomes t = h w rounded; the largest |t| and its remainder: max|h w| = mx + me
+      float mx = 0.f, me = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float t = f[i][j] * w[j], e = fmaf(fabsf(f[i][j]), fabsf(w[j]), -fabsf(t));
-        if (fabsf(t) > mx) {
-          mx = fabsf(t);
-          me = e;
-        }
-        f[i][j] = t;
-      }
-    }
-  }
-  row_max_pair<TPR>(mx, me, red[1][group], red[2][group], group, li);
-  const float amax = mx * rstd;                             // max|y|; NaN if the row holds NaN or infinity
-  const float top = amax < kScaleFloor ? kScaleFloor : amax;
-  // the short way where neither 448 / max|h w| nor the floor matters
-  const bool direct = amax >= kScaleFloor && mx >= kScaleFloor;
-  const float k2 = kE4m3Max / (direct ? mx : top);
-  if (!direct) {   // t 448 / max|h w| = (t r) 448 / top
+      for (int i = 0; i < VPT; ++i) {
+        const int v = li + i * TPR;
+        if (on(r, v)) {
+          float w[8];
+          load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] *= rstd;
-  }
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = li + i * TPR;
-    if (v < nv) {
-      bool near = false;
-      float q[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        q[j] = f[i][j] * k2;
-        // within 8 units of a tie of the 3-bit mantissa; the four roundings above are worth 4 at most
-        near |= (__float_as_uint(q[j]) << 12) - ((0x80000u - 8u) << 12) <= 16u << 12;
-      }
-      if (near && direct) {   // 1 vector in 8000
-        const float k2lo = (fmaf(-k2, mx, kE4m3Max) - k2 * me) / mx;
-        float h[8], w[8];
-        if (RES) Vec<HT>::widen(Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v), h);
-        else Vec<XT>::widen(Vec<XT>::load(static_cast<const XT*>(p.x) + base + 8 * v), h);
-        load_w(p.w, p.w_bf16, 8 * v, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float t = f[i][j], hi = t * k2;
-          q[j] = round_to_odd(hi, fmaf(t, k2, -hi) + fmaf(t, k2lo, fmaf(h[j], w[j], -t) * k2));
+          for (int j = 0; j < 8; ++j) {
+            const float h = f[r][i][j], t = h * w[j], e = fmaf(fabsf(h), fabsf(w[j]), -fabsf(t));
+            if (fabsf(t) > mx) {
+              mx = fabsf(t);
+              me = e;
+            }
+            f[r][i][j] = t;
+          }
         }
       }
-      Vec<YT>::store(static_cast<YT*>(p.y) + base + 8 * v, q);
+      row_max_pair<TPR>(mx, me, red[1][group], red[2][group], group, li);
+      const float amax = mx * rstd[r];                          // max|y|; NaN if the row holds NaN or infinity
+      const float top = amax < kScaleFloor ? kScaleFloor : amax;
+      // the short way where neither 448 / max|h w| nor the floor matters
+      const bool direct = amax >= kScaleFloor && mx >= kScaleFloor;
+      const float k2 = kE4m3Max / (direct ? mx : top);
+      if (!direct) {   // t 448 / max|h w| = (t r) 448 / top
+#pragma unroll
+        for (int i = 0; i < VPT; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) f[r][i][j] *= rstd[r];
+      }
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const int v = li + i * TPR;
+        if (on(r, v)) {
+          bool near = false;
+          float q[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            q[j] = f[r][i][j] * k2;
+            // within 8 units of a tie of the 3-bit mantissa; the four roundings above are worth 4 at most
+            near |= (__float_as_uint(q[j]) << 12) - ((0x80000u - 8u) << 12) <= 16u << 12;
+          }
+          if (near && direct) {   // 1 vector in 8000
+            const float k2lo = (fmaf(-k2, mx, kE4m3Max) - k2 * me) / mx;
+            float h[8], w[8];
+            if (RES) Vec<HT>::widen(Vec<HT>::load(static_cast<const HT*>(p.h) + at(r, v)), h);
+            else Vec<XT>::widen(Vec<XT>::load(static_cast<const XT*>(p.x) + at(r, v)), h);
+            load_w(p.w, p.w_bf16, 8 * v, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float t = f[r][i][j], hi = t * k2;
+              q[j] = round_to_odd(hi, fmaf(t, k2, -hi) + fmaf(t, k2lo, fmaf(h[j], w[j], -t) * k2));
+            }
+          }
+          Vec<YT>::store(static_cast<YT*>(p.y) + at(r, v), q);
+        }
+      }
+      if (li == 0 && row0 + r < p.N) p.scale[row0 + r] = top / kE4m3Max;
     }
   }
-  if (li == 0) p.scale[row] = top / kE4m3Max;
 }
 
 struct BwdParams {
@@ -471,16 +493,22 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restri
 }
 
 // Forward layout (threads a row, vectors a thread): the first whose capacity
-// holds the row, so that few lanes idle.  For few rows (up to `wide_rows`, the
+// holds the row, so that few lanes idle.  For few rows (up to the
 // SM count) a row's own latency counts, not the lanes left idle, so wider rows
 // are taken, up to one vector a thread (1 x 5120: 2.5 against 3.1 us, most of it
 // the launch, 148 x 5120: 2.9 against 3.7; 300 x 5120: 5.9 against 4.4).
-inline int pick_config(int d, int64_t N, int wide_rows) {
+// Short rows of many (more than 64 per SM) go four at a time, up to 128 elements
+// also two or four of them to a warp's width (393,120 heads of 128, bf16: 35
+// against 81 us of a row a warp, one at a time; 100,000 x 256: 33.2 against
+// 36.3, but 46.2 against 43.9 to e4m3, where the arithmetic of a row counts;
+// 60,000 x 512: no difference).
+inline int pick_config(int d, int64_t N, int sms, bool quant) {
   static const int cap[6] = {32 * 3, 64 * 3, 64 * 5, 128 * 5, 256 * 5, 512 * 5};
   const int nv = d >> 3;
+  if (nv <= (quant ? 16 : 32) && N > 64 * (int64_t)sms) return nv <= 8 ? 6 : nv <= 16 ? 7 : 8;
   int i = 0;
   while (cap[i] < nv) ++i;
-  if (N <= wide_rows) {
+  if (N <= sms) {
     static const int one[6] = {32, 64, 64, 128, 256, 512};
     while (i < 5 && one[i] < nv) ++i;
   }
@@ -496,19 +524,28 @@ inline int sm_count_of_current() {
 
 template <class XT, class HT, bool RES, class YT>
 static moga_status launch_fwd(const FwdParams& p, cudaStream_t s) {
-  switch (pick_config(p.d, p.N, sm_count_of_current())) {
-#define MOGA_NORM_CASE(I, TPR, VPT)                                                                            \
+  switch (pick_config(p.d, p.N, sm_count_of_current(), sizeof(YT) == 1)) {
+#define MOGA_NORM_CASE(I, TPR, VPT, ROWS)                                                                      \
   case I: {                                                                                                    \
-    constexpr int g = kCtaThreads<TPR> / TPR;                                                                \
-    rms_norm_kernel<TPR, VPT, XT, HT, RES, YT><<<(p.N - 1) / g + 1, kCtaThreads<TPR>, 0, s>>>(p);            \
+    constexpr int g = kCtaThreads<TPR> / TPR * ROWS;                                                           \
+    rms_norm_kernel<TPR, VPT, ROWS, XT, HT, RES, YT><<<(p.N - 1) / g + 1, kCtaThreads<TPR>, 0, s>>>(p);        \
     break;                                                                                                     \
   }
-    MOGA_NORM_CASE(0, 32, 3)
-    MOGA_NORM_CASE(1, 64, 3)
-    MOGA_NORM_CASE(2, 64, 5)
-    MOGA_NORM_CASE(3, 128, 5)
-    MOGA_NORM_CASE(4, 256, 5)
-    MOGA_NORM_CASE(5, 512, 5)
+    MOGA_NORM_CASE(0, 32, 3, 1)
+    MOGA_NORM_CASE(1, 64, 3, 1)
+    MOGA_NORM_CASE(2, 64, 5, 1)
+    MOGA_NORM_CASE(3, 128, 5, 1)
+    MOGA_NORM_CASE(4, 256, 5, 1)
+    MOGA_NORM_CASE(5, 512, 5, 1)
+    MOGA_NORM_CASE(6, 8, 1, 4)
+    MOGA_NORM_CASE(7, 16, 1, 4)
+    default: {
+      if constexpr (sizeof(YT) > 1) {
+        constexpr int g = 8 * 4;
+        rms_norm_kernel<32, 1, 4, XT, HT, RES, YT><<<(p.N - 1) / g + 1, 256, 0, s>>>(p);
+      }
+      break;
+    }
 #undef MOGA_NORM_CASE
   }
   return check_launch("moga_rms_norm");

@@ -24,7 +24,9 @@ def _rand(torch, dev, shape, dt, seed, scale=1.0):
 # one width per thread layout and its borders, the widest, and the least; N of one row, of one CTA's rows and a
 # rest, and above the SM count (where the layout for few rows ends)
 SHAPES = [(1, 8), (5, 64), (149, 136), (3, 768), (300, 776), (1, 1536), (301, 1544), (3, 2560), (150, 2568), (1, 5120),
-          (151, 5128), (2, 10240), (149, 10248), (1, 16384), (150, 16384)]
+          (151, 5128), (2, 10240), (149, 10248), (1, 16384), (150, 16384),
+          # many short rows, several at a time
+          (9500, 8), (9473, 64), (9999, 128), (9481, 136), (9490, 256), (9475, 264), (9500, 512)]
 TYPES = [("bf16", None, "bf16"), ("bf16", None, "e4m3"), ("f32", None, "f32"), ("f32", None, "bf16"),
          ("f32", None, "e4m3"), ("bf16", "bf16", "bf16"), ("bf16", "bf16", "e4m3"), ("bf16", "f32", "bf16"),
          ("bf16", "f32", "f32"), ("bf16", "f32", "e4m3"), ("f32", "f32", "f32"), ("f32", "f32", "bf16"),
