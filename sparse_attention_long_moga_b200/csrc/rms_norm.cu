@@ -325,20 +325,29 @@ struct BwdParams {
 // dw in registers (each thread always sees the same columns), then adds its
 // row groups in shared memory and writes one partial row.  No atomics: every
 // sum runs in a fixed order, so dw is the same from run to run.
-// GROUPS rows at a time, VPT vectors a thread.  Rows of up to 768 elements: a
-// warp a row, 8 rows a CTA.  Wider rows: a row a CTA of just enough threads, so
-// that an SM holds many rows in different phases and the loads of some are
-// under way while others are at their sums (bwd_shape).  63,960 x 1536, bf16
-// dy, fp32 h: 233 us, 6.7 TB/s, against 276 us of four rows a CTA with three
-// vectors a thread; bf16 h: 129 us, 6.1 TB/s.
-template <int GROUPS, int VPT, class DT, class HT, bool AHEAD = false>
-__global__ void __launch_bounds__(GROUPS > 1 ? 32 * GROUPS
-                                  : !AHEAD && (VPT == 1 || (VPT == 2 && sizeof(HT) == 2)) ? 1024 : 512)
+// TPR threads a row (0: the CTA), VPT vectors a thread.  Rows of up to 768
+// elements: a warp a row, 8 rows a CTA; of up to 128 and 64, half and a quarter
+// of a warp, so that no lane is idle.  Wider rows: a row a CTA of just enough
+// threads, so that an SM holds many rows in different phases and the loads of
+// some are under way while others are at their sums (bwd_shape).  63,960 x
+// 1536, bf16 dy, fp32 h: 233 us, 6.7 TB/s, against 276 us of four rows a CTA
+// with three vectors a thread; bf16 h: 129 us, 6.1 TB/s.  393,120 heads of 128,
+// bf16: 64 us, of 64: 35 us, against 129 and 127 us of a warp a row.
+template <int TPR, int VPT, class DT, class HT, bool AHEAD = false>
+__global__ void __launch_bounds__(TPR > 0 ? 256
+                                  : !AHEAD && (VPT == 1 || (VPT == 2 && sizeof(HT) == 2)) ? 1024
+                                  : !AHEAD && VPT == 2 ? 640 : 512,
+                                  TPR > 0 && VPT == 1 ? 3 : 1)
 rms_norm_bwd_kernel(const BwdParams p) {
+  constexpr int GROUPS = TPR > 0 ? 256 / TPR : 1;
   extern __shared__ float s_dw[];                 // [d] when there is more than one group
   __shared__ float2 red[2][32];
-  const int tpr = GROUPS > 1 ? 32 : blockDim.x;
-  const int group = GROUPS > 1 ? threadIdx.x / 32 : 0, li = GROUPS > 1 ? threadIdx.x % 32 : threadIdx.x;
+  const int tpr = TPR > 0 ? TPR : blockDim.x;
+  const int group = TPR > 0 ? threadIdx.x / tpr : 0, li = TPR > 0 ? threadIdx.x % tpr : threadIdx.x;
+  // rows of a warp's width of threads and less: the warp's rows go through the
+  // loop together, those past the last one as zeros
+  constexpr int kInWarp = TPR > 0 && TPR < 32 ? 32 / TPR : 1;
+  const int sub = group % kInWarp;
   const int nv = p.d >> 3;
   float acc[VPT][8];
 #pragma unroll
@@ -353,7 +362,7 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = li + i * tpr;
-      if (v < nv) {
+      if (v < nv && (kInWarp == 1 || row < p.N)) {
         dt[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
         ht[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
         if (p.dres) st[i] = Vec<HT>::load(static_cast<const HT*>(p.dres) + base + 8 * v);
@@ -365,8 +374,9 @@ rms_norm_bwd_kernel(const BwdParams p) {
     if (blockIdx.x * GROUPS + group < p.N) load(blockIdx.x * GROUPS + group, dn, hn, sn);
   }
   int par = 0;
-  for (int row = blockIdx.x * GROUPS + group; row < p.N; row += gridDim.x * GROUPS, par ^= 1) {
+  for (int row = blockIdx.x * GROUPS + group; row - sub < p.N; row += gridDim.x * GROUPS, par ^= 1) {
     const size_t base = (size_t)row * p.d;
+    const bool in = kInWarp == 1 || row < p.N;
     typename Vec<DT>::type dv[VPT];
     typename Vec<HT>::type hv[VPT], sv[VPT];
     if constexpr (AHEAD) {
@@ -381,7 +391,7 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = li + i * tpr;
-        if (v < nv) {
+        if (v < nv && in) {
           dv[i] = Vec<DT>::load(static_cast<const DT*>(p.dy) + base + 8 * v);
           hv[i] = Vec<HT>::load(static_cast<const HT*>(p.h) + base + 8 * v);
           if (p.dres) sv[i] = Vec<HT>::load(static_cast<const HT*>(p.dres) + base + 8 * v);
@@ -392,7 +402,7 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = li + i * tpr;
-      if (v < nv) {
+      if (v < nv && in) {
         float dy[8], h[8], w[8];
         Vec<DT>::widen(dv[i], dy);
         Vec<HT>::widen(hv[i], h);
@@ -404,9 +414,9 @@ rms_norm_bwd_kernel(const BwdParams p) {
         }
       }
     }
-    ss = warp_sum(ss);
-    dot = warp_sum(dot);
-    if (GROUPS == 1) {   // both sums of the CTA's warps cross one barrier; the slots alternate, so one is enough
+    ss = warp_sum<(TPR > 0 ? TPR : 32)>(ss);
+    dot = warp_sum<(TPR > 0 ? TPR : 32)>(dot);
+    if (TPR == 0) {   // both sums of the CTA's warps cross one barrier; the slots alternate, so one is enough
       if ((threadIdx.x & 31) == 0) red[par][threadIdx.x >> 5] = make_float2(ss, dot);
       __syncthreads();
       const bool on = (threadIdx.x & 31) < (blockDim.x >> 5);
@@ -420,7 +430,7 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = li + i * tpr;
-      if (v < nv) {
+      if (v < nv && in) {
         float dy[8], h[8], w[8], o[8];
         Vec<DT>::widen(dv[i], dy);
         Vec<HT>::widen(hv[i], h);
@@ -443,8 +453,17 @@ rms_norm_bwd_kernel(const BwdParams p) {
   }
   if (!p.partial) return;
   float* dst = p.partial + (size_t)blockIdx.x * p.d;
-  for (int g = 0; g < GROUPS; ++g) {
-    if (group == g) {
+  if constexpr (kInWarp > 1) {   // the warp's rows first, then its TPR lanes stand for it
+#pragma unroll
+    for (int o = 16; o >= TPR; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < VPT; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], o);
+  }
+  constexpr int kParts = TPR > 0 ? 8 : 1;
+  for (int g = 0; g < kParts; ++g) {
+    if (group == g * kInWarp) {
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = li + i * tpr;
@@ -455,11 +474,11 @@ rms_norm_bwd_kernel(const BwdParams p) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) acc[i][j] += s[j];
           }
-          Vec<float>::store(g == GROUPS - 1 ? dst + 8 * v : s_dw + 8 * v, acc[i]);
+          Vec<float>::store(g == kParts - 1 ? dst + 8 * v : s_dw + 8 * v, acc[i]);
         }
       }
     }
-    if (GROUPS > 1) __syncthreads();
+    if (kParts > 1) __syncthreads();
   }
 }
 
@@ -561,8 +580,13 @@ static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_
 
 // Backward launch shape: threads of a CTA, vectors a thread, CTAs an SM holds.
 // All CTAs have to be resident at once (a second round of them costs a third),
-// so the last follows from the kernels' registers: 64 (one vector; two with a
-// bf16 h), up to 100 (two, fp32 h), 128 (three, four), 80 (warp a row, one).
+// so the last follows from the kernels' registers, which their launch bounds
+// hold: 64 (one vector; two with a bf16 h), 96 (two, fp32 h), 128 (three, four),
+// 80 (a warp a row or less, one).
+// Short rows keep the next one under way, but for a warp's width of fp32 h,
+// where registers spill and enough bytes are on their way without (256
+// columns: bf16 h 73 against 84 us for 200,000 rows, fp32 249 against 238 us
+// for 400,000).
 // Bytes on the way decide between one and two vectors: two where a bf16 row's
 // vectors are small or where one would leave an SM's threads unused
 // (32,760 x 5120, fp32 h: 526 us with one vector, 367 with two).
@@ -575,8 +599,9 @@ struct BwdShape {
   bool ahead;
 };
 constexpr int kWarpRow = 768;
+inline int bwd_rows(int d) { return d <= 64 ? 32 : d <= 128 ? 16 : d <= kWarpRow ? 8 : 1; }   // of a CTA
 inline BwdShape bwd_shape(int d, bool h_f32) {
-  if (d <= 256) return {256, 1, 3, false};
+  if (d <= 256) return {256, 1, 3, !h_f32 || d <= 128};
   if (d <= kWarpRow) return {256, 3, 2, false};
   auto threads = [d](int vpt) { return (ceil_div(d / 8, vpt) + 31) / 32 * 32; };
   const int t1 = threads(1), t2 = threads(2);
@@ -587,7 +612,7 @@ inline BwdShape bwd_shape(int d, bool h_f32) {
   return {t2, 2, std::max(1, 640 / t2), false};
 }
 inline int bwd_ctas(int64_t N, int d, bool h_f32, int sms) {
-  const int rows = d <= kWarpRow ? 8 : 1;
+  const int rows = bwd_rows(d);
   return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * bwd_shape(d, h_f32).per_sm);
 }
 
@@ -595,13 +620,15 @@ template <class DT, class HT>
 static moga_status launch_bwd(const BwdParams& p, int ctas, cudaStream_t s) {
   const BwdShape k = bwd_shape(p.d, sizeof(HT) == 4);
   const size_t smem = p.d * sizeof(float);
-  if (p.d <= 256) rms_norm_bwd_kernel<8, 1, DT, HT><<<ctas, k.threads, smem, s>>>(p);
-  else if (p.d <= kWarpRow) rms_norm_bwd_kernel<8, 3, DT, HT><<<ctas, k.threads, smem, s>>>(p);
-  else if (k.vpt == 2 && !k.ahead) rms_norm_bwd_kernel<1, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
-  else if constexpr (sizeof(HT) == 2) rms_norm_bwd_kernel<1, 2, DT, HT, true><<<ctas, k.threads, 0, s>>>(p);
+  if (p.d <= 64) rms_norm_bwd_kernel<8, 1, DT, HT, true><<<ctas, k.threads, smem, s>>>(p);
+  else if (p.d <= 128) rms_norm_bwd_kernel<16, 1, DT, HT, true><<<ctas, k.threads, smem, s>>>(p);
+  else if (p.d <= 256) rms_norm_bwd_kernel<32, 1, DT, HT, sizeof(HT) == 2><<<ctas, k.threads, smem, s>>>(p);
+  else if (p.d <= kWarpRow) rms_norm_bwd_kernel<32, 3, DT, HT><<<ctas, k.threads, smem, s>>>(p);
+  else if (k.vpt == 2 && !k.ahead) rms_norm_bwd_kernel<0, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+  else if constexpr (sizeof(HT) == 2) rms_norm_bwd_kernel<0, 2, DT, HT, true><<<ctas, k.threads, 0, s>>>(p);
   else if constexpr (sizeof(HT) == 4) {
-    if (k.vpt == 1) rms_norm_bwd_kernel<1, 1, DT, HT><<<ctas, k.threads, 0, s>>>(p);
-    else rms_norm_bwd_kernel<1, 4, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+    if (k.vpt == 1) rms_norm_bwd_kernel<0, 1, DT, HT><<<ctas, k.threads, 0, s>>>(p);
+    else rms_norm_bwd_kernel<0, 4, DT, HT><<<ctas, k.threads, 0, s>>>(p);
   }
   return check_launch("moga_rms_norm_bwd");
 }

@@ -52,6 +52,22 @@ def test_forward_matches_oracle(x_dt, r_dt, out, cuda_device):
         check_norm_y(_np(y.float()), None if scale is None else _np(scale), want, out)
 
 
+@pytest.mark.parametrize("h_dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,d", [(30001, 8), (15003, 40), (15001, 64), (29999, 64), (14999, 104), (15002, 128),
+                                 (7501, 200), (7499, 256)])
+def test_backward_of_short_rows_many_rounds(N, d, h_dt, cuda_device):
+    """Several rows a warp, several rounds, and a last round that some of a warp's rows are not in."""
+    import torch
+    import sparse_attention_long_moga_b200 as moga
+    h = _rand(torch, cuda_device, (N, d), h_dt, 10, 3.0)
+    dy = _rand(torch, cuda_device, (N, d), "bf16", 11)
+    dres = _rand(torch, cuda_device, (N, d), h_dt, 12)
+    w = _rand(torch, cuda_device, (d,), "f32", 13)
+    dx, dw, _ = moga.moga_rms_norm_backward(dy, h, w, dres=dres, eps=EPS)
+    moga.device_status()
+    check_norm_backward(_np(dx), _np(dw), _np(dy), _np(h), _np(w), _np(dres), EPS, h_dt)
+
+
 @pytest.mark.parametrize("dy_dt,h_dt", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")])
 @pytest.mark.parametrize("with_dres", [False, True])
 def test_backward_matches_oracle(dy_dt, h_dt, with_dres, cuda_device):
