@@ -593,7 +593,8 @@ static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_
 // A bf16 row's vectors are small: where 512 threads fill up, they keep the next
 // row's under way as well (at 110 registers; 63,960 x 1536: 129 against 138 us
 // with 1024 threads that do not, 20,000 x 8192: 210 against 231; 5120, of whose
-// 320-thread CTAs only one would fit: 266 against 236).
+// 320-thread CTAs only one would fit: 266 against 236).  So do the fp32 rows of
+// which an SM holds one either way (20,000 x 8192, bf16 dy: 380 against 464 us).
 struct BwdShape {
   int threads, vpt, per_sm;
   bool ahead;
@@ -605,7 +606,7 @@ inline BwdShape bwd_shape(int d, bool h_f32) {
   if (d <= kWarpRow) return {256, 3, 2, false};
   auto threads = [d](int vpt) { return (ceil_div(d / 8, vpt) + 31) / 32 * 32; };
   const int t1 = threads(1), t2 = threads(2);
-  if (!h_f32 && t2 <= 512 && 512 / t2 * t2 >= 448) return {t2, 2, 512 / t2, true};
+  if ((!h_f32 || t2 >= 448) && t2 <= 512 && 512 / t2 * t2 >= 448) return {t2, 2, 512 / t2, true};
   if (!h_f32) return {t2, 2, std::max(1, 1024 / t2), false};
   if (d > 8192) return {threads(4), 4, std::max(1, 512 / threads(4)), false};
   if (1024 / t1 * t1 >= 896) return {t1, 1, 1024 / t1, false};
@@ -625,7 +626,7 @@ static moga_status launch_bwd(const BwdParams& p, int ctas, cudaStream_t s) {
   else if (p.d <= 256) rms_norm_bwd_kernel<32, 1, DT, HT, sizeof(HT) == 2><<<ctas, k.threads, smem, s>>>(p);
   else if (p.d <= kWarpRow) rms_norm_bwd_kernel<32, 3, DT, HT><<<ctas, k.threads, smem, s>>>(p);
   else if (k.vpt == 2 && !k.ahead) rms_norm_bwd_kernel<0, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
-  else if constexpr (sizeof(HT) == 2) rms_norm_bwd_kernel<0, 2, DT, HT, true><<<ctas, k.threads, 0, s>>>(p);
+  else if (k.vpt == 2) rms_norm_bwd_kernel<0, 2, DT, HT, true><<<ctas, k.threads, 0, s>>>(p);
   else if constexpr (sizeof(HT) == 4) {
     if (k.vpt == 1) rms_norm_bwd_kernel<0, 1, DT, HT><<<ctas, k.threads, 0, s>>>(p);
     else rms_norm_bwd_kernel<0, 4, DT, HT><<<ctas, k.threads, 0, s>>>(p);

@@ -54,9 +54,9 @@ def test_forward_matches_oracle(x_dt, r_dt, out, cuda_device):
 
 @pytest.mark.parametrize("h_dt", ["bf16", "f32"])
 @pytest.mark.parametrize("N,d", [(30001, 8), (15003, 40), (15001, 64), (29999, 64), (14999, 104), (15002, 128),
-                                 (7501, 200), (7499, 256)])
-def test_backward_of_short_rows_many_rounds(N, d, h_dt, cuda_device):
-    """Several rows a warp, several rounds, and a last round that some of a warp's rows are not in."""
+                                 (7501, 200), (7499, 256), (701, 7176), (700, 8192)])
+def test_backward_of_many_rounds(N, d, h_dt, cuda_device):
+    """Several rounds: of several rows a warp, the last without some of them, and of one row an SM."""
     import torch
     import sparse_attention_long_moga_b200 as moga
     h = _rand(torch, cuda_device, (N, d), h_dt, 10, 3.0)
