@@ -470,6 +470,10 @@ moga_status moga_rms_norm(const void* x, moga_dtype x_dt, const void* residual, 
  * ws:        moga_rms_norm_bwd_ws_bytes(N, d) bytes of scratch (unused, may be
  *            NULL, where dw is NULL)
  * fp32 dy with a bf16 h is MOGA_ERR_UNSUPPORTED; limits as for the forward.
+ * A NaN in a row of h or dy, or an infinity in h, makes its row of dx NaN (and dw
+ * where it reaches); a row whose sum of squares passes the fp32 range adds
+ * nothing to dw and has dx = dres, y being constant there.  The sum of dy w h
+ * over a row stays within the fp32 range too, else its dx is NaN.
  * Deterministic: every sum runs in a fixed order. */
 size_t moga_rms_norm_bwd_ws_bytes(int64_t N, int32_t d);
 moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const void* h, moga_dtype h_dt, const void* w,

@@ -11,8 +11,8 @@
 // mantissa; the few values that fall near one are computed again in two fp32
 // words, so that q is the e4m3 value nearest to the exact ratio.
 //
-// Backward, with dn = dy * w and c = r^2 * mean(dn * h):
-//   dx = r * (dn - h * c) + dres,   dw = sum over rows of dy * h * r
+// Backward, with dn = dy * w and n = h * r:
+//   dx = r * (dn - n * mean(dn * n)) + dres,   dw = sum over rows of dy * n
 // r is recomputed: the row is in registers anyway, so nothing is saved but h.
 //
 // Bound: HBM.  Each row is read once into registers (8-element vectors, one
@@ -426,7 +426,10 @@ rms_norm_bwd_kernel(const BwdParams p) {
     }
     const float inv_d = 1.f / (float)p.d;
     const float rstd = 1.f / sqrtf(ss * inv_d + p.eps);
-    const float c = rstd * rstd * rstd * (dot * inv_d);
+    // r (dn - n mean(dn n)) as r dn - n c, c = r mean(dn n): no power of r is
+    // formed, so nothing leaves the fp32 range before the result does (r^3 would
+    // for rows of rms 4e12 and more and for an eps of 1e-26 and less)
+    const float c = rstd * (rstd * (dot * inv_d));
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
       const int v = li + i * tpr;
@@ -437,8 +440,9 @@ rms_norm_bwd_kernel(const BwdParams p) {
         load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          o[j] = rstd * (dy[j] * w[j]) - c * h[j];
-          acc[i][j] += dy[j] * h[j] * rstd;
+          const float n = h[j] * rstd;
+          acc[i][j] += dy[j] * n;
+          o[j] = rstd * (dy[j] * w[j]) - n * c;
         }
         if (p.dres) {
           float s[8];
