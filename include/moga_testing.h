@@ -58,6 +58,12 @@
  * the pair takes them, out[10i .. 10i+9] = (pair, kind (0 gated tile, 1 dx tile,
  * 2 dW unit), up matrix, row tile, column tile, split, first k stage, end k
  * stage, first 256-row half of the tile, end half).  Host code only.
+ *
+ * moga_test_norm_bwd_ctas(d, h_dt, dy_dt, resident) returns the CTAs an SM
+ * that the launch of moga_rms_norm_bwd asks for with rows of d elements and
+ * enough of them (all have to be resident at once), -1 for arguments that the
+ * call would reject, and writes how many the current device holds for that
+ * kernel.  Launches nothing.
  */
 #ifndef MOGA_TESTING_H
 #define MOGA_TESTING_H
@@ -79,6 +85,7 @@ int32_t moga_test_bwd_units(int32_t mode, int32_t keys, const int32_t* cu_seqlen
 
 int64_t moga_test_ffn_units(int32_t grad, int64_t N, int32_t d, int32_t F, int32_t need_dx, int32_t need_dw,
                             int32_t bn, int32_t sms, int32_t* out, int64_t cap);
+int64_t moga_test_norm_bwd_ctas(int32_t d, moga_dtype h_dt, moga_dtype dy_dt, int32_t* resident);
 
 #ifdef __cplusplus
 }

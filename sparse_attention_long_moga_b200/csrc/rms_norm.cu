@@ -321,6 +321,15 @@ struct BwdParams {
   bool w_bf16;
 };
 
+// Residence of the backward's forms, which the kernel's launch bounds and the
+// launch rule (bwd_shape) both take from here.  Of the forms with a warp a row
+// or less (256 threads) an SM holds this many CTAs,
+__host__ __device__ constexpr int bwd_warp_ctas(int vpt) { return vpt == 1 ? 3 : 2; }
+// and of those with a row a CTA as many as these threads make up.
+__host__ __device__ constexpr int bwd_sm_threads(int vpt, bool h_f32, bool ahead) {
+  return vpt == 4 || ahead ? 512 : vpt == 2 && h_f32 ? 640 : 1024;
+}
+
 // Persistent: a CTA walks its rows with a fixed stride and keeps its share of
 // dw in registers (each thread always sees the same columns), then adds its
 // row groups in shared memory and writes one partial row.  No atomics: every
@@ -334,10 +343,8 @@ struct BwdParams {
 // with three vectors a thread; bf16 h: 129 us, 6.1 TB/s.  393,120 heads of 128,
 // bf16: 64 us, of 64: 35 us, against 129 and 127 us of a warp a row.
 template <int TPR, int VPT, class DT, class HT, bool AHEAD = false>
-__global__ void __launch_bounds__(TPR > 0 ? 256
-                                  : !AHEAD && (VPT == 1 || (VPT == 2 && sizeof(HT) == 2)) ? 1024
-                                  : !AHEAD && VPT == 2 ? 640 : 512,
-                                  TPR > 0 && VPT == 1 ? 3 : 1)
+__global__ void __launch_bounds__(TPR > 0 ? 256 : bwd_sm_threads(VPT, sizeof(HT) == 4, AHEAD),
+                                  TPR > 0 ? bwd_warp_ctas(VPT) : 1)
 rms_norm_bwd_kernel(const BwdParams p) {
   constexpr int GROUPS = TPR > 0 ? 256 / TPR : 1;
   extern __shared__ float s_dw[];                 // [d] when there is more than one group
@@ -584,9 +591,12 @@ static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_
 
 // Backward launch shape: threads of a CTA, vectors a thread, CTAs an SM holds.
 // All CTAs have to be resident at once (a second round of them costs a third),
-// so the last follows from the kernels' registers, which their launch bounds
-// hold: 64 (one vector; two with a bf16 h), 96 (two, fp32 h), 128 (three, four),
-// 80 (a warp a row or less, one).
+// so the last is what the kernels' launch bounds hold their registers to
+// (bwd_warp_ctas, bwd_sm_threads): 64 a thread (one vector; two with a bf16 h),
+// 96 (two, fp32 h), 128 (three, four, and with the next row under way), 80 (a
+// warp a row or less, one).  Without a bound three vectors with an fp32 h take
+// 138 to 152, one CTA an SM and a second round (40,000 rows, bf16 dy, of 264:
+// 61 against 42 us, of 512: 70 against 52, of 768: 88 against 73).
 // Short rows keep the next one under way, but for a warp's width of fp32 h,
 // where registers spill and enough bytes are on their way without (256
 // columns: bf16 h 73 against 84 us for 200,000 rows, fp32 249 against 238 us
@@ -598,7 +608,8 @@ static moga_status launch_fwd_y(const FwdParams& p, moga_dtype y_dt, cudaStream_
 // row's under way as well (at 110 registers; 63,960 x 1536: 129 against 138 us
 // with 1024 threads that do not, 20,000 x 8192: 210 against 231; 5120, of whose
 // 320-thread CTAs only one would fit: 266 against 236).  So do the fp32 rows of
-// which an SM holds one either way (20,000 x 8192, bf16 dy: 380 against 464 us).
+// which an SM holds one either way (20,000 x 8192, bf16 dy: 367 against 466 us;
+// fp32 dy: 474 against 472 with dres, 411 against 442 without).
 struct BwdShape {
   int threads, vpt, per_sm;
   bool ahead;
@@ -606,35 +617,45 @@ struct BwdShape {
 constexpr int kWarpRow = 768;
 inline int bwd_rows(int d) { return d <= 64 ? 32 : d <= 128 ? 16 : d <= kWarpRow ? 8 : 1; }   // of a CTA
 inline BwdShape bwd_shape(int d, bool h_f32) {
-  if (d <= 256) return {256, 1, 3, !h_f32 || d <= 128};
-  if (d <= kWarpRow) return {256, 3, 2, false};
+  if (d <= 256) return {256, 1, bwd_warp_ctas(1), !h_f32 || d <= 128};
+  if (d <= kWarpRow) return {256, 3, bwd_warp_ctas(3), false};
   auto threads = [d](int vpt) { return (ceil_div(d / 8, vpt) + 31) / 32 * 32; };
   const int t1 = threads(1), t2 = threads(2);
-  if ((!h_f32 || t2 >= 448) && t2 <= 512 && 512 / t2 * t2 >= 448) return {t2, 2, 512 / t2, true};
-  if (!h_f32) return {t2, 2, std::max(1, 1024 / t2), false};
-  if (d > 8192) return {threads(4), 4, std::max(1, 512 / threads(4)), false};
-  if (1024 / t1 * t1 >= 896) return {t1, 1, 1024 / t1, false};
-  return {t2, 2, std::max(1, 640 / t2), false};
+  auto shape = [h_f32](int threads, int vpt, bool ahead) {
+    return BwdShape{threads, vpt, std::max(1, bwd_sm_threads(vpt, h_f32, ahead) / threads), ahead};
+  };
+  if ((!h_f32 || t2 >= 448) && t2 <= 512 && 512 / t2 * t2 >= 448) return shape(t2, 2, true);
+  if (!h_f32) return shape(t2, 2, false);
+  if (d > 8192) return shape(threads(4), 4, false);
+  if (1024 / t1 * t1 >= 896) return shape(t1, 1, false);
+  return shape(t2, 2, false);
 }
 inline int bwd_ctas(int64_t N, int d, bool h_f32, int sms) {
   const int rows = bwd_rows(d);
   return (int)std::min<int64_t>((N + rows - 1) / rows, (int64_t)sms * bwd_shape(d, h_f32).per_sm);
 }
 
+// the kernel of bwd_shape's form
+template <class DT, class HT>
+static auto bwd_kernel(int d) -> void (*)(const BwdParams) {
+  const BwdShape k = bwd_shape(d, sizeof(HT) == 4);
+  if (d <= 64) return rms_norm_bwd_kernel<8, 1, DT, HT, true>;
+  if (d <= 128) return rms_norm_bwd_kernel<16, 1, DT, HT, true>;
+  if (d <= 256) return rms_norm_bwd_kernel<32, 1, DT, HT, sizeof(HT) == 2>;
+  if (d <= kWarpRow) return rms_norm_bwd_kernel<32, 3, DT, HT>;
+  if constexpr (sizeof(HT) == 4) {
+    if (k.vpt == 1) return rms_norm_bwd_kernel<0, 1, DT, HT>;
+    if (k.vpt == 4) return rms_norm_bwd_kernel<0, 4, DT, HT>;
+  }
+  return k.ahead ? rms_norm_bwd_kernel<0, 2, DT, HT, true> : rms_norm_bwd_kernel<0, 2, DT, HT>;
+}
+
+// its columns' sums, shared by a CTA's rows where it has several
+inline size_t bwd_smem(int d) { return d <= kWarpRow ? d * sizeof(float) : 0; }
+
 template <class DT, class HT>
 static moga_status launch_bwd(const BwdParams& p, int ctas, cudaStream_t s) {
-  const BwdShape k = bwd_shape(p.d, sizeof(HT) == 4);
-  const size_t smem = p.d * sizeof(float);
-  if (p.d <= 64) rms_norm_bwd_kernel<8, 1, DT, HT, true><<<ctas, k.threads, smem, s>>>(p);
-  else if (p.d <= 128) rms_norm_bwd_kernel<16, 1, DT, HT, true><<<ctas, k.threads, smem, s>>>(p);
-  else if (p.d <= 256) rms_norm_bwd_kernel<32, 1, DT, HT, sizeof(HT) == 2><<<ctas, k.threads, smem, s>>>(p);
-  else if (p.d <= kWarpRow) rms_norm_bwd_kernel<32, 3, DT, HT><<<ctas, k.threads, smem, s>>>(p);
-  else if (k.vpt == 2 && !k.ahead) rms_norm_bwd_kernel<0, 2, DT, HT><<<ctas, k.threads, 0, s>>>(p);
-  else if (k.vpt == 2) rms_norm_bwd_kernel<0, 2, DT, HT, true><<<ctas, k.threads, 0, s>>>(p);
-  else if constexpr (sizeof(HT) == 4) {
-    if (k.vpt == 1) rms_norm_bwd_kernel<0, 1, DT, HT><<<ctas, k.threads, 0, s>>>(p);
-    else rms_norm_bwd_kernel<0, 4, DT, HT><<<ctas, k.threads, 0, s>>>(p);
-  }
+  bwd_kernel<DT, HT>(p.d)<<<ctas, bwd_shape(p.d, sizeof(HT) == 4).threads, bwd_smem(p.d), s>>>(p);
   return check_launch("moga_rms_norm_bwd");
 }
 
@@ -745,4 +766,20 @@ extern "C" moga_status moga_rms_norm_bwd(const void* dy, moga_dtype dy_dt, const
   if (st != MOGA_OK || !dw) return st;
   rms_norm_dw_kernel<<<ceil_div(d, 32), dim3(32, 32), 0, s>>>(p.partial, ctas, d, dw);
   return check_launch("moga_rms_norm_bwd/dw");
+}
+
+// test hook (moga_testing.h): CTAs an SM asked for, and resident
+extern "C" int64_t moga_test_norm_bwd_ctas(int32_t d, moga_dtype h_dt, moga_dtype dy_dt, int32_t* resident) {
+  using namespace moga;
+  using namespace moga::norm;
+  if (check_dims("moga_test_norm_bwd_ctas", 1, d, 1.f) != MOGA_OK || !is_float_dt(h_dt) || !is_float_dt(dy_dt) ||
+      (dy_dt == MOGA_F32 && h_dt == MOGA_BF16))
+    return -1;
+  using B = __nv_bfloat16;
+  const BwdShape k = bwd_shape(d, h_dt == MOGA_F32);
+  auto* f = h_dt == MOGA_BF16 ? bwd_kernel<B, B>(d) : dy_dt == MOGA_BF16 ? bwd_kernel<B, float>(d) : bwd_kernel<float, float>(d);
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, k.threads, bwd_smem(d)) != cudaSuccess) return -1;
+  *resident = n;
+  return k.per_sm;
 }

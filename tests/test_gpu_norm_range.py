@@ -1,4 +1,7 @@
-"""GPU: the norm's backward on rows of extreme magnitude (oracle and tolerances: _block.py)."""
+"""GPU: the norm's backward on rows of extreme magnitude and its launches' residence (oracle and tolerances:
+_block.py)."""
+import ctypes
+
 import numpy as np
 import pytest
 
@@ -81,3 +84,20 @@ def test_backward_of_exceptional_rows(dy_dt, h_dt, cuda_device):
         dx1, dw1, _ = moga.moga_rms_norm_backward(dy[good].contiguous(), h[good].contiguous(), w,
                                                   dres=dres[good].contiguous())
         assert torch.equal(dx[good], dx1) and torch.isfinite(dw1).all()
+
+
+def test_backward_launches_are_resident(cuda_device):
+    """All CTAs of a backward launch fit the SMs at once, at every width and type."""
+    import torch  # noqa: F401  (the context)
+    import sparse_attention_long_moga_b200 as moga
+    fn = moga._lib.lib().moga_test_norm_bwd_ctas
+    fn.restype = ctypes.c_int64
+    fn.argtypes = [ctypes.c_int32] * 3 + [ctypes.POINTER(ctypes.c_int32)]
+    n = ctypes.c_int32(0)
+    bad = []
+    for h_dt, dy_dt in ((1, 1), (0, 1), (0, 0)):
+        for d in range(8, 16385, 8):
+            want = fn(d, h_dt, dy_dt, ctypes.byref(n))
+            if not 1 <= want <= n.value:
+                bad.append((d, h_dt, dy_dt, want, n.value))
+    assert not bad, (len(bad), bad[:5])
