@@ -9,7 +9,9 @@
 // y / scale = (h w) * 448 / max|h w| (r cancels).  A value that fp32 puts on
 // the wrong side of a rounding border is off by a whole step of the 3-bit
 // mantissa; the few values that fall near one are computed again in two fp32
-// words, so that q is the e4m3 value nearest to the exact ratio.
+// words, so that q is the e4m3 value nearest to the exact ratio (where that is
+// a normal value, and but for rows with max|y| below 2^-100 or max|h w| outside
+// 2^-80 to 2^80, where the second word may be cut short).
 //
 // Backward, with dn = dy * w and n = h * r:
 //   dx = r * (dn - n * mean(dn * n)) + dres,   dw = sum over rows of dy * n
@@ -47,17 +49,18 @@ template <> struct Vec<__nv_bfloat16> {
       f[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
     }
   }
-  // rounds to nearest even; f becomes the stored value
-  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) {
+  // rounds to nearest even
+  static __device__ __forceinline__ type narrow(const float* f) {
     uint32_t u[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
       u[i] = *reinterpret_cast<const uint32_t*>(&b);
     }
-    *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
+    return make_uint4(u[0], u[1], u[2], u[3]);
   }
-  static __device__ __forceinline__ float round(float f) { return __bfloat162float(__float2bfloat16_rn(f)); }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const type& t) { *reinterpret_cast<uint4*>(p) = t; }
+  static __device__ __forceinline__ void store(__nv_bfloat16* p, const float* f) { store(p, narrow(f)); }
 };
 template <> struct Vec<float> {
   struct type { float4 a, b; };
@@ -68,11 +71,14 @@ template <> struct Vec<float> {
     f[0] = t.a.x; f[1] = t.a.y; f[2] = t.a.z; f[3] = t.a.w;
     f[4] = t.b.x; f[5] = t.b.y; f[6] = t.b.z; f[7] = t.b.w;
   }
-  static __device__ __forceinline__ void store(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  static __device__ __forceinline__ type narrow(const float* f) {
+    return {make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7])};
   }
-  static __device__ __forceinline__ float round(float f) { return f; }
+  static __device__ __forceinline__ void store(float* p, const type& t) {
+    *reinterpret_cast<float4*>(p) = t.a;
+    *reinterpret_cast<float4*>(p + 4) = t.b;
+  }
+  static __device__ __forceinline__ void store(float* p, const float* f) { store(p, narrow(f)); }
 };
 template <> struct Vec<__nv_fp8_e4m3> {
   // values already scaled into +-448; out of range saturates, NaN stays NaN
@@ -124,33 +130,31 @@ __device__ __forceinline__ float row_sum(float v, float* slots, int group, int l
   return r;
 }
 
-// The largest mx over the TPR threads of a row, with the me that goes with it
-// (the larger one where several share mx).
+// The largest v over the TPR threads of a row (slots as above).
 template <int TPR>
-__device__ __forceinline__ void row_max_pair(float& mx, float& me, float* slots, float* slots_e, int group,
-                                             int lane_in_row) {
+__device__ __forceinline__ float row_max(float v, float* slots, int group, int lane_in_row) {
 #pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, mx, o), e2 = __shfl_xor_sync(0xffffffffu, me, o);
-    if (m2 > mx || (m2 == mx && e2 > me)) {
-      mx = m2;
-      me = e2;
-    }
-  }
-  if (TPR <= 32) return;
-  if ((lane_in_row & 31) == 0) {
-    slots[lane_in_row >> 5] = mx;
-    slots_e[lane_in_row >> 5] = me;
-  }
+  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  if (TPR <= 32) return v;
+  if ((lane_in_row & 31) == 0) slots[lane_in_row >> 5] = v;
   row_sync<TPR>(group);
-  mx = slots[0];
-  me = slots_e[0];
+  v = slots[0];
 #pragma unroll
-  for (int i = 1; i < TPR / 32; ++i)
-    if (slots[i] > mx || (slots[i] == mx && slots_e[i] > me)) {
-      mx = slots[i];
-      me = slots_e[i];
-    }
+  for (int i = 1; i < TPR / 32; ++i) v = fmaxf(v, slots[i]);
+  return v;
+}
+
+// Whether any thread of the row has v not 0; rows inside a warp: any of the warp.
+template <int TPR>
+__device__ __forceinline__ bool row_any(uint32_t v, int group) {
+  if (TPR <= 32) return __any_sync(0xffffffffu, v != 0);
+  uint32_t r;
+  asm volatile(
+      "{ .reg .pred p, q; setp.ne.u32 p, %1, 0; bar.red.or.pred q, %2, %3, p; selp.u32 %0, 1, 0, q; }"
+      : "=r"(r)
+      : "r"(v), "r"(1 + group), "n"(TPR)
+      : "memory");
+  return r != 0;
 }
 
 // hi + lo (|lo| below an ulp or so of hi) as one fp32 value that a later
@@ -162,6 +166,10 @@ __device__ __forceinline__ float round_to_odd(float hi, float lo) {
   if (rest != 0.f && !(b & 1)) b += (rest > 0.f) == (s > 0.f) ? 1 : -1;
   return __int_as_float(b);
 }
+
+// bits of q past a tie of the 3-bit mantissa, wrapped: at most 16 << 12 within 8 units of one
+__device__ __forceinline__ uint32_t past_tie(float q) { return (__float_as_uint(q) << 12) - ((0x80000u - 8u) << 12); }
+constexpr uint32_t kNearTie = 16u << 12;
 
 struct FwdParams {
   const void *x, *res, *w;
@@ -176,9 +184,12 @@ template <int TPR>
 constexpr int kCtaThreads = TPR > 256 ? TPR : 256;
 
 // ROWS rows at a time per TPR threads: short rows need several under way per
-// thread to fill the memory's latency.
+// thread to fill the memory's latency.  The e4m3 forms of three vectors ask for
+// the four CTAs an SM that their 54 to 64 registers allow: left alone the
+// compiler takes 48 and more instructions (32,760 x 1536, bf16 + bf16: 86
+// against 82 us).
 template <int TPR, int VPT, int ROWS, class XT, class HT, bool RES, class YT>
-__global__ void __launch_bounds__(kCtaThreads<TPR>)
+__global__ void __launch_bounds__(kCtaThreads<TPR>, sizeof(YT) == 1 && VPT == 3 ? 4 : 0)
 rms_norm_kernel(const FwdParams p) {
   static_assert(TPR <= 32 || ROWS == 1, "rows that share a barrier go one at a time");
   constexpr int kGroups = kCtaThreads<TPR> / TPR;
@@ -219,8 +230,10 @@ rms_norm_kernel(const FwdParams p) {
           float t[8];
           Vec<HT>::widen(rv[r][i], t);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) f[r][i][j] = Vec<HT>::round(f[r][i][j] + t[j]);
-          Vec<HT>::store(static_cast<HT*>(p.h) + at(r, v), f[r][i]);
+          for (int j = 0; j < 8; ++j) f[r][i][j] += t[j];
+          const typename Vec<HT>::type stored = Vec<HT>::narrow(f[r][i]);
+          Vec<HT>::store(static_cast<HT*>(p.h) + at(r, v), stored);
+          Vec<HT>::widen(stored, f[r][i]);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) ss += f[r][i][j] * f[r][i][j];
@@ -248,8 +261,8 @@ rms_norm_kernel(const FwdParams p) {
   } else {
 #pragma unroll
     for (int r = 0; r < ROWS; ++r) {
-      // f becomes t = h w rounded; the largest |t| and its remainder: max|h w| = mx + me
-      float mx = 0.f, me = 0.f;
+      // f becomes t = h w rounded
+      float mine = 0.f;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = li + i * TPR;
@@ -258,16 +271,12 @@ rms_norm_kernel(const FwdParams p) {
           load_w(p.w, p.w_bf16, 8 * v, w);
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            const float h = f[r][i][j], t = h * w[j], e = fmaf(fabsf(h), fabsf(w[j]), -fabsf(t));
-            if (fabsf(t) > mx) {
-              mx = fabsf(t);
-              me = e;
-            }
-            f[r][i][j] = t;
+            f[r][i][j] *= w[j];
+            mine = fmaxf(mine, fabsf(f[r][i][j]));
           }
         }
       }
-      row_max_pair<TPR>(mx, me, red[1][group], red[2][group], group, li);
+      const float mx = row_max<TPR>(mine, red[1][group], group, li);
       const float amax = mx * rstd[r];                          // max|y|; NaN if the row holds NaN or infinity
       const float top = amax < kScaleFloor ? kScaleFloor : amax;
       // the short way where neither 448 / max|h w| nor the floor matters
@@ -279,31 +288,55 @@ rms_norm_kernel(const FwdParams p) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) f[r][i][j] *= rstd[r];
       }
+      uint32_t near = 0;   // vectors with a value near a tie
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         const int v = li + i * TPR;
         if (on(r, v)) {
-          bool near = false;
           float q[8];
+          uint32_t past = ~0u;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             q[j] = f[r][i][j] * k2;
-            // within 8 units of a tie of the 3-bit mantissa; the four roundings above are worth 4 at most
-            near |= (__float_as_uint(q[j]) << 12) - ((0x80000u - 8u) << 12) <= 16u << 12;
+            // the four roundings above (t, mx, 448 / mx, q) are worth 4 units at most
+            past = min(past, past_tie(q[j]));
           }
-          if (near && direct) {   // 1 vector in 8000
-            const float k2lo = (fmaf(-k2, mx, kE4m3Max) - k2 * me) / mx;
-            float h[8], w[8];
-            if (RES) Vec<HT>::widen(Vec<HT>::load(static_cast<const HT*>(p.h) + at(r, v)), h);
-            else Vec<XT>::widen(Vec<XT>::load(static_cast<const XT*>(p.x) + at(r, v)), h);
-            load_w(p.w, p.w_bf16, 8 * v, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float t = f[r][i][j], hi = t * k2;
-              q[j] = round_to_odd(hi, fmaf(t, k2, -hi) + fmaf(t, k2lo, fmaf(h[j], w[j], -t) * k2));
-            }
-          }
+          near |= (past <= kNearTie ? 1u : 0u) << i;
           Vec<YT>::store(static_cast<YT*>(p.y) + at(r, v), q);
+        }
+      }
+      if (!direct) near = 0;
+      if (row_any<TPR>(near, group)) {   // 1 vector in 8000: in two words, max|h w| = mx + me
+        auto reload = [&](int i, float* h, float* w) {   // vector i of this thread
+          const int v = li + i * TPR;
+          if (RES) Vec<HT>::widen(Vec<HT>::load(static_cast<const HT*>(p.h) + at(r, v)), h);
+          else Vec<XT>::widen(Vec<XT>::load(static_cast<const XT*>(p.x) + at(r, v)), h);
+          load_w(p.w, p.w_bf16, 8 * v, w);
+        };
+        float h[8], w[8], me = -mx;
+        if (direct && mine == mx) {   // this thread has the largest product, or one of several
+#pragma unroll 1
+          for (int i = 0; i < VPT && on(r, li + i * TPR); ++i) {
+            reload(i, h, w);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (fabsf(h[j] * w[j]) == mx) me = fmaxf(me, fmaf(fabsf(h[j]), fabsf(w[j]), -mx));
+          }
+        }
+        me = row_max<TPR>(me, red[2][group], group, li);
+        const float k2lo = (fmaf(-k2, mx, kE4m3Max) - k2 * me) / mx;
+#pragma unroll 1
+        for (; near; near &= near - 1) {
+          const int i = __ffs(near) - 1;
+          reload(i, h, w);
+          float q[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t = h[j] * w[j], hi = t * k2;
+            const float lo = fmaf(t, k2, -hi) + fmaf(t, k2lo, fmaf(h[j], w[j], -t) * k2);
+            q[j] = lo == 0.f ? hi : round_to_odd(hi, lo);   // a zero keeps its sign
+          }
+          Vec<YT>::store(static_cast<YT*>(p.y) + at(r, li + i * TPR), q);
         }
       }
       if (li == 0 && row0 + r < p.N) p.scale[row0 + r] = top / kE4m3Max;

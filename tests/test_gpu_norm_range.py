@@ -1,5 +1,5 @@
-"""GPU: the norm's backward on rows of extreme magnitude and its launches' residence (oracle and tolerances:
-_block.py)."""
+"""GPU: the norm's backward on rows of extreme magnitude and its launches' residence, the e4m3 output next to its
+rounding borders (oracle and tolerances: _block.py)."""
 import ctypes
 
 import numpy as np
@@ -7,6 +7,7 @@ import pytest
 
 from _block import check_norm_backward
 from _block import to_np as _np
+from oracle import block
 
 pytestmark = pytest.mark.gpu
 
@@ -101,3 +102,91 @@ def test_backward_launches_are_resident(cuda_device):
             if not 1 <= want <= n.value:
                 bad.append((d, h_dt, dy_dt, want, n.value))
     assert not bad, (len(bad), bad[:5])
+
+
+# ------------------------------------------------------- e4m3: values next to a rounding border
+
+NORMAL_TIES = np.concatenate([(2 * (8 + np.arange(8)) + 1) * 2.0 ** (e - 3) / 2 for e in range(-6, 9)])
+NORMAL_TIES = NORMAL_TIES[NORMAL_TIES < 448]
+
+
+def _nearest(hw, top):
+    """(lower, upper) e4m3 values that hw 448 / top may round to, equal but at an exact tie.  hw and top are products
+    of two fp32 values, so |hw| 448 and tie top are exact in float64 and their order decides."""
+    a = np.abs(hw)
+    v = a * 448.0 / top
+    step = 2 * block.e4m3_half_step(v)
+    lo = np.floor(v / step) * step
+    left, right = a * 448.0, (lo + step / 2) * top
+    return np.where(left > right, lo + step, lo), np.where(left < right, lo, lo + step)
+
+
+def _check_nearest(moga, torch, dev, h, w, copies=1):
+    ht = torch.from_numpy(np.tile(h, (copies, 1))).to(dev)
+    q, _, _ = moga.moga_rms_norm(ht, torch.from_numpy(w).to(dev), out_dtype=torch.float8_e4m3fn)
+    moga.device_status()
+    hw = h.astype(np.float64) * w.astype(np.float64)
+    lo, hi = _nearest(hw, np.max(np.abs(hw), axis=1, keepdims=True))
+    got = np.abs(_np(q.float()))[:len(h)]
+    assert torch.equal(q.view(torch.uint8).view(copies, len(h), -1)[-1], q.view(torch.uint8)[:len(h)])
+    bad = (got < lo) | (got > hi)
+    assert not bad.any(), "%d of %d" % (bad.sum(), bad.size)
+
+
+def _near(ties, top, w, ulps):
+    """fp32 h with h w within some ulps of tie top / 448."""
+    c = (ties * top / 448 / w).astype(np.float32)
+    return (c.view(np.int32) + ulps).view(np.float32)
+
+
+@pytest.mark.parametrize("weighted", [False, True])
+@pytest.mark.parametrize("d,copies", [(120, 1), (120, 200), (248, 200), (1024, 1), (1024, 6), (2048, 3), (5120, 2)])
+@pytest.mark.parametrize("ties", [NORMAL_TIES], ids=["normal"])
+def test_e4m3_nearest_value(ties, d, copies, weighted, cuda_device):
+    """Values within two fp32 steps of a tie, whose fp32 product often lies on its other side."""
+    import torch
+    import sparse_attention_long_moga_b200 as moga
+    rng = np.random.default_rng(d + copies)
+    h = np.empty((64, d), dtype=np.float32)
+    w = rng.uniform(0.5, 2, d).astype(np.float32) if weighted else np.ones(d, dtype=np.float32)
+    for r in range(64):
+        h[r, 0] = rng.uniform(4, 8)        # the largest product: no tie reaches it
+        w[0] = 2 if weighted else 1
+        top = float(h[r, 0]) * float(w[0])
+        t = rng.choice(ties, d - 1)
+        h[r, 1:] = _near(t, top, w[1:].astype(np.float64), rng.integers(-2, 3, d - 1).astype(np.int32))
+        h[r, 1:] *= rng.choice([-1, 1], d - 1).astype(np.float32)
+        h[r, rng.integers(1, d, d // 16)] = 0
+    _check_nearest(moga, torch, cuda_device, h, w, copies)
+
+
+def _equal_products(rng):
+    """(h1, w1, h2, w2): products that round to one fp32 value, the second exact one the larger by half a step."""
+    while True:
+        h1, w1 = (rng.uniform(1.5, 2, 4000).astype(np.float32) for _ in range(2))
+        w2 = rng.uniform(1.5, 2, 4000).astype(np.float32)
+        t = h1 * w1
+        h2 = t / w2
+        e1, e2 = (h.astype(np.float64) * w - t.astype(np.float64) for h, w in ((h1, w1), (h2, w2)))
+        ulp = np.spacing(t)
+        ok = np.nonzero((h2 * w2 == t) & (e1 < -0.3 * ulp) & (e2 > 0.3 * ulp))[0]
+        if len(ok):
+            i = ok[0]
+            return h1[i], w1[i], h2[i], w2[i]
+
+
+@pytest.mark.parametrize("order", [0, 1])
+def test_e4m3_of_equal_largest_products(order, cuda_device):
+    """Two products of one thread that round to the same fp32 value: the exactly larger one is the row's maximum."""
+    import torch
+    import sparse_attention_long_moga_b200 as moga
+    rng = np.random.default_rng(order)
+    d = 2048
+    for _ in range(24):
+        h1, w1, h2, w2 = _equal_products(rng)
+        h, w = np.empty((1, d), dtype=np.float32), np.ones(d, dtype=np.float32)
+        a, b = (2, 6) if order == 0 else (6, 2)
+        top = float(h2) * float(w2)
+        h[0] = _near(rng.choice(NORMAL_TIES, d), top, 1.0, rng.integers(-1, 2, d).astype(np.int32))
+        h[0, a], w[a], h[0, b], w[b] = h1, w1, h2, w2
+        _check_nearest(moga, torch, cuda_device, h, w)
