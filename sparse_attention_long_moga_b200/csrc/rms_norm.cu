@@ -9,9 +9,10 @@
 // y / scale = (h w) * 448 / max|h w| (r cancels).  A value that fp32 puts on
 // the wrong side of a rounding border is off by a whole step of the 3-bit
 // mantissa; the few values that fall near one are computed again in two fp32
-// words, so that q is the e4m3 value nearest to the exact ratio (where that is
-// a normal value, and but for rows with max|y| below 2^-100 or max|h w| outside
-// 2^-80 to 2^80, where the second word may be cut short).
+// words, so that q is the e4m3 value nearest to the exact ratio (but for rows
+// with max|y| below 2^-100 or max|h w| outside 2^-80 to 2^80, where the second
+// word may be cut short).  The second words need the remainder of the largest
+// product; the row's threads look for it only where a value is near a border.
 //
 // Backward, with dn = dy * w and n = h * r:
 //   dx = r * (dn - n * mean(dn * n)) + dres,   dw = sum over rows of dy * n
@@ -170,6 +171,7 @@ __device__ __forceinline__ float round_to_odd(float hi, float lo) {
 // bits of q past a tie of the 3-bit mantissa, wrapped: at most 16 << 12 within 8 units of one
 __device__ __forceinline__ uint32_t past_tie(float q) { return (__float_as_uint(q) << 12) - ((0x80000u - 8u) << 12); }
 constexpr uint32_t kNearTie = 16u << 12;
+constexpr float kE4m3Normal = 0.015625f;   // 2^-6, the least normal value
 
 struct FwdParams {
   const void *x, *res, *w;
@@ -293,14 +295,22 @@ rms_norm_kernel(const FwdParams p) {
       for (int i = 0; i < VPT; ++i) {
         const int v = li + i * TPR;
         if (on(r, v)) {
-          float q[8];
+          float q[8], least = kE4m3Normal;
           uint32_t past = ~0u;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             q[j] = f[r][i][j] * k2;
             // the four roundings above (t, mx, 448 / mx, q) are worth 4 units at most
             past = min(past, past_tie(q[j]));
+            least = fminf(least, fabsf(q[j]));
           }
+          // Subnormal values are spaced as those of [2^-6, 2^-5): with 2^-6 added, whose unit is at
+          // least twice theirs (their 4 are 2, and the sum's own rounding half a one), their ties
+          // are ties of the mantissa.
+          if (least < kE4m3Normal)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (fabsf(q[j]) < kE4m3Normal) past = min(past, past_tie(fabsf(q[j]) + kE4m3Normal));
           near |= (past <= kNearTie ? 1u : 0u) << i;
           Vec<YT>::store(static_cast<YT*>(p.y) + at(r, v), q);
         }
@@ -810,7 +820,9 @@ extern "C" int64_t moga_test_norm_bwd_ctas(int32_t d, moga_dtype h_dt, moga_dtyp
     return -1;
   using B = __nv_bfloat16;
   const BwdShape k = bwd_shape(d, h_dt == MOGA_F32);
-  auto* f = h_dt == MOGA_BF16 ? bwd_kernel<B, B>(d) : dy_dt == MOGA_BF16 ? bwd_kernel<B, float>(d) : bwd_kernel<float, float>(d);
+  auto* f = h_dt == MOGA_BF16    ? bwd_kernel<B, B>(d)
+            : dy_dt == MOGA_BF16 ? bwd_kernel<B, float>(d)
+                                 : bwd_kernel<float, float>(d);
   int n = 0;
   if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, k.threads, bwd_smem(d)) != cudaSuccess) return -1;
   *resident = n;

@@ -106,6 +106,7 @@ def test_backward_launches_are_resident(cuda_device):
 
 # ------------------------------------------------------- e4m3: values next to a rounding border
 
+SUBNORMAL_TIES = (2 * np.arange(8) + 1) * 2.0 ** -10
 NORMAL_TIES = np.concatenate([(2 * (8 + np.arange(8)) + 1) * 2.0 ** (e - 3) / 2 for e in range(-6, 9)])
 NORMAL_TIES = NORMAL_TIES[NORMAL_TIES < 448]
 
@@ -141,7 +142,7 @@ def _near(ties, top, w, ulps):
 
 @pytest.mark.parametrize("weighted", [False, True])
 @pytest.mark.parametrize("d,copies", [(120, 1), (120, 200), (248, 200), (1024, 1), (1024, 6), (2048, 3), (5120, 2)])
-@pytest.mark.parametrize("ties", [NORMAL_TIES], ids=["normal"])
+@pytest.mark.parametrize("ties", [SUBNORMAL_TIES, NORMAL_TIES], ids=["subnormal", "normal"])
 def test_e4m3_nearest_value(ties, d, copies, weighted, cuda_device):
     """Values within two fp32 steps of a tie, whose fp32 product often lies on its other side."""
     import torch
