@@ -439,7 +439,8 @@ moga_status moga_balance_loss_part(const int32_t* counts, const void* route_ws, 
  * and stands for y_q * scale.  A NaN in h makes its whole row of y NaN, an
  * infinity its own value (and the others 0); in e4m3 the scale of such a row is
  * NaN (where w is not 0).  A row whose sum of squares passes the fp32 range
- * gives zeros.
+ * gives zeros.  With an e4m3 y the products h * w stay within that range, else
+ * the row's scale is infinite or NaN.
  * x:        [N][d], x_dt (MOGA_F32 or MOGA_BF16)
  * residual: [N][d], res_dt, or NULL.  Pairs (x, residual): bf16 + bf16,
  *           bf16 + fp32, fp32 + fp32; fp32 + bf16 is MOGA_ERR_UNSUPPORTED

@@ -191,3 +191,21 @@ def test_e4m3_of_equal_largest_products(order, cuda_device):
         h[0] = _near(rng.choice(NORMAL_TIES, d), top, 1.0, rng.integers(-1, 2, d).astype(np.int32))
         h[0, a], w[a], h[0, b], w[b] = h1, w1, h2, w2
         _check_nearest(moga, torch, cuda_device, h, w)
+
+
+def test_e4m3_products_past_the_range(cuda_device):
+    """Where h w passes the fp32 range the row's scale says so (infinite or NaN); its neighbours are untouched."""
+    import torch
+    import sparse_attention_long_moga_b200 as moga
+    for N, d in ((5, 1536), (9500, 64)):
+        h = torch.randn((N, d), generator=torch.Generator(device=cuda_device).manual_seed(d), device=cuda_device)
+        h[1] *= 1e17          # the sum of squares stays in the range, the products do not
+        h[3] = 3e38           # neither does
+        w = torch.full((d,), 2.0, device=cuda_device)
+        w[5] = 1e23
+        good = [r for r in range(N) if r not in (1, 3)]
+        q, _, s = moga.moga_rms_norm(h, w, out_dtype=torch.float8_e4m3fn)
+        q1, _, s1 = moga.moga_rms_norm(h[good].contiguous(), w, out_dtype=torch.float8_e4m3fn)
+        moga.device_status()
+        assert not torch.isfinite(s[[1, 3]]).any()
+        assert torch.equal(s[good], s1) and torch.equal(q.view(torch.uint8)[good], q1.view(torch.uint8))
