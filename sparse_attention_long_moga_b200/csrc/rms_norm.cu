@@ -573,12 +573,11 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restri
 // Short rows of many (more than 64 per SM) go four at a time, up to 128 elements
 // also two or four of them to a warp's width (393,120 heads of 128, bf16: 35
 // against 81 us of a row a warp, one at a time; 100,000 x 256: 33.2 against
-// 36.3, but 46.2 against 43.9 to e4m3, where the arithmetic of a row counts;
-// 60,000 x 512: no difference).
-inline int pick_config(int d, int64_t N, int sms, bool quant) {
+// 36.3, to e4m3 32.2 against 39.5; 60,000 x 512: no difference).
+inline int pick_config(int d, int64_t N, int sms) {
   static const int cap[6] = {32 * 3, 64 * 3, 64 * 5, 128 * 5, 256 * 5, 512 * 5};
   const int nv = d >> 3;
-  if (nv <= (quant ? 16 : 32) && N > 64 * (int64_t)sms) return nv <= 8 ? 6 : nv <= 16 ? 7 : 8;
+  if (nv <= 32 && N > 64 * (int64_t)sms) return nv <= 8 ? 6 : nv <= 16 ? 7 : 8;
   int i = 0;
   while (cap[i] < nv) ++i;
   if (N <= sms) {
@@ -597,7 +596,7 @@ inline int sm_count_of_current() {
 
 template <class XT, class HT, bool RES, class YT>
 static moga_status launch_fwd(const FwdParams& p, cudaStream_t s) {
-  switch (pick_config(p.d, p.N, sm_count_of_current(), sizeof(YT) == 1)) {
+  switch (pick_config(p.d, p.N, sm_count_of_current())) {
 #define MOGA_NORM_CASE(I, TPR, VPT, ROWS)                                                                      \
   case I: {                                                                                                    \
     constexpr int g = kCtaThreads<TPR> / TPR * ROWS;                                                           \
@@ -612,13 +611,7 @@ static moga_status launch_fwd(const FwdParams& p, cudaStream_t s) {
     MOGA_NORM_CASE(5, 512, 5, 1)
     MOGA_NORM_CASE(6, 8, 1, 4)
     MOGA_NORM_CASE(7, 16, 1, 4)
-    default: {
-      if constexpr (sizeof(YT) > 1) {
-        constexpr int g = 8 * 4;
-        rms_norm_kernel<32, 1, 4, XT, HT, RES, YT><<<(p.N - 1) / g + 1, 256, 0, s>>>(p);
-      }
-      break;
-    }
+    MOGA_NORM_CASE(8, 32, 1, 4)
 #undef MOGA_NORM_CASE
   }
   return check_launch("moga_rms_norm");
