@@ -21,9 +21,11 @@
 // Bound: HBM.  Each row is read once into registers (8-element vectors, one
 // to five per thread) and written once; sums, the row statistics and dw are
 // fp32.  TPR threads share a row, 256 / TPR rows share a CTA.  32,760 x 1536,
-// bf16 + bf16 to bf16: 61 us, 6.6 TB/s; 32,760 x 5120, bf16 + fp32 to e4m3:
-// 284 us, 6.5 TB/s (300 in long runs, where the chip is at its power cap and
-// instructions cost bandwidth: hence the tie check in two of them).
+// bf16 + bf16 to bf16: 61 us, 6.6 TB/s (the last writes are still in L2 when it
+// ends); 32,760 x 5120, bf16 + fp32 to e4m3: 277 us, 6.6 TB/s (298 in long
+// runs, where the chip is at its power cap and instructions cost bandwidth:
+// hence the tie check in three of them, and all that follows from it only in
+// rows that have a value near a tie).
 #include <algorithm>
 
 #include <cuda_fp8.h>
@@ -384,7 +386,7 @@ __host__ __device__ constexpr int bwd_sm_threads(int vpt, bool h_f32, bool ahead
 // some are under way while others are at their sums (bwd_shape).  63,960 x
 // 1536, bf16 dy, fp32 h: 233 us, 6.7 TB/s, against 276 us of four rows a CTA
 // with three vectors a thread; bf16 h: 129 us, 6.1 TB/s.  393,120 heads of 128,
-// bf16: 64 us, of 64: 35 us, against 129 and 127 us of a warp a row.
+// bf16: 62 us, of 64: 34 us, against 129 and 127 us of a warp a row.
 template <int TPR, int VPT, class DT, class HT, bool AHEAD = false>
 __global__ void __launch_bounds__(TPR > 0 ? 256 : bwd_sm_threads(VPT, sizeof(HT) == 4, AHEAD),
                                   TPR > 0 ? bwd_warp_ctas(VPT) : 1)
@@ -546,7 +548,7 @@ __global__ void __launch_bounds__(1024) rms_norm_dw_kernel(const float* __restri
   if (c < d) {
     const float* q = partial + c;
     int r = j;
-    for (; r + 7 * 32 < rows; r += 8 * 32) {   // eight loads under way (up to 23 rows a slice)
+    for (; r + 7 * 32 < rows; r += 8 * 32) {   // eight loads under way (up to 37 rows a slice: 8 CTAs an SM)
       float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = q[(size_t)(r + 32 * i) * d];
